@@ -1,6 +1,6 @@
 """Build the CUDA library in-tree: recurrent_vision_backbone_b200/libgtr_gla.so.
 
-Compiles csrc/gtr_gla.cu for sm_100a only (nvcc cross-compiles without a GPU):
+Compiles the csrc/*.cu sources for sm_100a only (nvcc cross-compiles without a GPU):
     python -m recurrent_vision_backbone_b200.build [--verbose]
 """
 from __future__ import annotations
@@ -9,13 +9,16 @@ import os
 import shutil
 import subprocess
 import sys
+import tempfile
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
-SOURCES = [os.path.join(CSRC, "gtr_gla.cu")]
-DEPS = SOURCES + [os.path.join(CSRC, n) for n in ("sm100_ptx.cuh", "gla_fwd_span.cuh", "gla_fwd_pipe.cuh", "swiglu_gate.cuh", "gla_bwd.cuh")]
-DEPS += [os.path.join(ROOT, "include", n) for n in ("gtr_gla.h", "gtr_swiglu.h", "gtr_gla_bwd.h")]
+SOURCES = [os.path.join(CSRC, n) for n in ("gtr_gla.cu", "ssm.cu", "group_norm.cu")]
+DEPS = SOURCES + [os.path.join(CSRC, n) for n in ("sm100_ptx.cuh", "gla_fwd_span.cuh", "gla_fwd_pipe.cuh", "swiglu_gate.cuh", "gla_bwd.cuh",
+                                                  "ops_common.cuh", "causal_conv.cuh", "ssm_scan.cuh", "ssm_scan_bwd.cuh")]
+DEPS += [os.path.join(ROOT, "include", n) for n in ("gtr_gla.h", "gtr_swiglu.h", "gtr_gla_bwd.h", "gtr_ops.h", "gtr_ssm.h",
+                                                    "gtr_norm.h")]
 LIB = os.path.join(HERE, "libgtr_gla.so")
 
 
@@ -26,10 +29,17 @@ def nvcc_path() -> str:
     raise RuntimeError("nvcc not found")
 
 
-def nvcc_cmd(out: str = LIB, extra=()) -> list:
+def nvcc_cmd(out: str = LIB, extra=(), inputs=None) -> list:
+    """The command that compiles and links `inputs` (all sources by default) into `out`."""
     return [nvcc_path(), "-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo", "-O3",
             "-std=c++17", "--shared", "-Xcompiler", "-fPIC", "-I", os.path.join(ROOT, "include"),
-            *extra, *SOURCES, "-o", out, "-lcudart"]
+            *extra, *(SOURCES if inputs is None else inputs), "-o", out, "-lcudart"]
+
+
+def compile_cmd(src: str, obj: str, extra=()) -> list:
+    """The command that compiles one source (the options of nvcc_cmd)."""
+    return [nvcc_path(), "-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo", "-O3",
+            "-std=c++17", "-Xcompiler", "-fPIC", "-I", os.path.join(ROOT, "include"), *extra, "-c", src, "-o", obj]
 
 
 def is_stale(out: str = LIB) -> bool:
@@ -43,7 +53,13 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if force or is_stale():
         extra = ["-Xptxas", "-v"] if verbose else []
         tmp = LIB + ".tmp"
-        subprocess.run(nvcc_cmd(tmp, extra), check=True)
+        with tempfile.TemporaryDirectory() as work:   # the sources side by side, then one link
+            objs = [os.path.join(work, os.path.basename(s) + ".o") for s in SOURCES]
+            procs = [subprocess.Popen(compile_cmd(s, o, extra)) for s, o in zip(SOURCES, objs)]
+            codes = [p.wait() for p in procs]
+            if any(codes):
+                raise subprocess.CalledProcessError(max(codes, key=abs), "nvcc")
+            subprocess.run(nvcc_cmd(tmp, inputs=objs), check=True)
         os.replace(tmp, LIB)
     return LIB
 

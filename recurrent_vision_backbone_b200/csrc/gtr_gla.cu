@@ -163,6 +163,7 @@ namespace gtr {
 // the backward pass: its kernels, then (below) its C entry points
 #include "../../include/gtr_gla_bwd.h"
 #include "gla_bwd.cuh"
+#include "ops_common.cuh"
 
 namespace gtr {
 enum KernelKind { kSpan = 0, kSpanShort = 1, kSpanZ = 2, kSpanShortZ = 3, kPipe = 4, kPipeZ = 5, kKinds = 6 };
@@ -713,6 +714,8 @@ static gtr_status_t cuda_status(cudaError_t e) {
     cudaGetLastError();   // clear a non-sticky error
     return GTR_ERR_CUDA;
 }
+// the operators of ssm.cu and group_norm.cu report through the same error record
+gtr_status_t gtr::ops_cuda_status(cudaError_t e) { return cuda_status(e); }
 
 extern "C" gtr_status_t gtr_gla_fwd(const gtr_half_t *q, const gtr_half_t *k,
                                     const gtr_half_t *v, const gtr_half_t *g, int B, int heads,
@@ -1004,6 +1007,9 @@ extern "C" gtr_status_t gtr_gla_device_status(void *stream) {
     }
     unsigned word = 0;
     if (cudaMemcpyFromSymbol(&word, g_error_word, sizeof(word)) != cudaSuccess) return GTR_ERR_CUDA;
+    const unsigned ops_word = ssm_take_errors() | norm_take_errors();   // read and cleared
+    if (ops_word & kOpsErrCuda) return GTR_ERR_CUDA;
+    word |= ops_word;
     if (word == kErrRange) {
         const unsigned zero = 0;
         cudaMemcpyToSymbol(g_error_word, &zero, sizeof(zero));
@@ -1215,7 +1221,7 @@ extern "C" gtr_status_t gtr_gla_bwd(const gtr_half_t *q, const gtr_half_t *k, co
 }
 
 
-extern "C" const char *gtr_gla_version(void) { return "0.3.0"; }
+extern "C" const char *gtr_gla_version(void) { return "0.4.0"; }
 
 extern "C" const char *gtr_gla_last_error(void) {
     return g_last_cuda_error == cudaSuccess ? "no error" : cudaGetErrorString(g_last_cuda_error);

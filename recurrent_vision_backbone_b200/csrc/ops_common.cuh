@@ -1,0 +1,227 @@
+// ops_common.cuh -- what the operators around the token mixer share (ssm.cu, group_norm.cu):
+// 16-bit element access, scan walks, activations, and the host side of argument checks.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <nvtx3/nvToolsExt.h>
+
+#include <cstdint>
+
+#include "../../include/gtr_ops.h"
+
+namespace gtr {
+
+// Defined in gtr_gla.cu: keeps the error for gtr_gla_last_error and turns it into a status.
+gtr_status_t ops_cuda_status(cudaError_t e);
+// Error bits of one source file's kernels on the current device, read and cleared
+// (gtr_gla_device_status collects them). kOpsErrCuda: the word could not be read.
+constexpr unsigned kOpsErrRange = 2u, kOpsErrCuda = 0x80000000u;
+unsigned ssm_take_errors();
+unsigned norm_take_errors();
+
+namespace ops {
+
+struct NvtxRange {
+    explicit NvtxRange(const char *name) { nvtxRangePushA(name); }
+    ~NvtxRange() { nvtxRangePop(); }
+    NvtxRange(const NvtxRange &) = delete;
+    NvtxRange &operator=(const NvtxRange &) = delete;
+};
+
+// ------------------------------------------------------------------ elements
+template <typename T>
+struct Elem;
+template <>
+struct Elem<__half> {
+    static __device__ __forceinline__ float get(uint16_t r) { return __half2float(__ushort_as_half(r)); }
+    static __device__ __forceinline__ uint16_t put(float f) { return __half_as_ushort(__float2half_rn(f)); }
+    static __device__ __forceinline__ float2 get2(uint32_t r) {
+        return __half22float2(*reinterpret_cast<const __half2 *>(&r));
+    }
+    static __device__ __forceinline__ uint32_t put2(float a, float b) {
+        const __half2 h = __floats2half2_rn(a, b);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    }
+    // whether a result left the type's range (|f| above the largest fp16, or NaN); the
+    // running maximum of |f| is what is tested, which fmaxf would lose a NaN from
+    static __device__ __forceinline__ bool bad(float f) { return !(fabsf(f) <= 65504.f); }
+};
+template <>
+struct Elem<__nv_bfloat16> {
+    static __device__ __forceinline__ float get(uint16_t r) { return __uint_as_float((uint32_t)r << 16); }
+    static __device__ __forceinline__ uint16_t put(float f) { return __bfloat16_as_ushort(__float2bfloat16_rn(f)); }
+    static __device__ __forceinline__ float2 get2(uint32_t r) {
+        return make_float2(__uint_as_float(r << 16), __uint_as_float(r & 0xffff0000u));
+    }
+    static __device__ __forceinline__ uint32_t put2(float a, float b) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    }
+    static __device__ __forceinline__ bool bad(float) { return false; }   // bf16 holds what float32 holds
+};
+
+// V consecutive elements as raw words: V = 8 is one 16-byte access, 4 an 8-byte one, 2 a
+// 4-byte one, 1 two bytes.
+template <int V>
+struct Raw {
+    uint32_t w[V >= 2 ? V / 2 : 1];
+};
+template <int V>
+__device__ __forceinline__ Raw<V> load_raw(const uint16_t *p) {
+    Raw<V> r;
+    if constexpr (V == 8) {
+        const uint4 x = __ldg(reinterpret_cast<const uint4 *>(p));
+        r.w[0] = x.x, r.w[1] = x.y, r.w[2] = x.z, r.w[3] = x.w;
+    } else if constexpr (V == 4) {
+        const uint2 x = __ldg(reinterpret_cast<const uint2 *>(p));
+        r.w[0] = x.x, r.w[1] = x.y;
+    } else if constexpr (V == 2) {
+        r.w[0] = __ldg(reinterpret_cast<const uint32_t *>(p));
+    } else {
+        r.w[0] = __ldg(p);
+    }
+    return r;
+}
+template <int V>
+__device__ __forceinline__ void store_raw(uint16_t *p, const Raw<V> &r) {
+    if constexpr (V == 8)
+        *reinterpret_cast<uint4 *>(p) = make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]);
+    else if constexpr (V == 4)
+        *reinterpret_cast<uint2 *>(p) = make_uint2(r.w[0], r.w[1]);
+    else if constexpr (V == 2)
+        *reinterpret_cast<uint32_t *>(p) = r.w[0];
+    else
+        *p = (uint16_t)r.w[0];
+}
+template <int V>
+__device__ __forceinline__ Raw<V> zero_raw() {
+    Raw<V> r;
+#pragma unroll
+    for (auto &x : r.w) x = 0u;   // +0 in both types
+    return r;
+}
+template <typename T, int V>
+__device__ __forceinline__ void unpack(const Raw<V> &r, float (&f)[V]) {
+    if constexpr (V == 1) {
+        f[0] = Elem<T>::get((uint16_t)r.w[0]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) {
+            const float2 v = Elem<T>::get2(r.w[i]);
+            f[2 * i] = v.x;
+            f[2 * i + 1] = v.y;
+        }
+    }
+}
+template <typename T, int V>
+__device__ __forceinline__ Raw<V> pack(const float (&f)[V]) {
+    Raw<V> r;
+    if constexpr (V == 1) {
+        r.w[0] = Elem<T>::put(f[0]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) r.w[i] = Elem<T>::put2(f[2 * i], f[2 * i + 1]);
+    }
+    return r;
+}
+
+// ------------------------------------------------------------------ functions
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+__device__ __forceinline__ float ex2(float x) {   // 2^x, about 2 ulp; 0 below 2^-126
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// e^x for x <= 0 with x log2(e) kept in two parts, so that a large |x| costs no accuracy
+__device__ __forceinline__ float exp_neg(float x) {
+    const float t = x * kLog2e;
+    const float lo = fmaf(x, kLog2e, -t) + x * 1.925963033e-8f;   // log2(e) - its float32 value
+    const float e = ex2(t);
+    return t < -126.f ? e : fmaf(e * kLn2, lo, e);
+}
+// log(1 + e) for e in [0, 1]: e times a polynomial of degree 10, interpolating log(1 + e) / e at
+// Chebyshev nodes (relative error 8.5e-10; 1.2e-7 evaluated in float32)
+__device__ __forceinline__ float log1p_01(float e) {
+    float p = 0.001986696617677808f;
+    p = fmaf(p, e, -0.013187826611101627f);
+    p = fmaf(p, e, 0.04100657254457474f);
+    p = fmaf(p, e, -0.08188040554523468f);
+    p = fmaf(p, e, 0.12377995997667313f);
+    p = fmaf(p, e, -0.16087622940540314f);
+    p = fmaf(p, e, 0.19885820150375366f);
+    p = fmaf(p, e, -0.24986496567726135f);
+    p = fmaf(p, e, 0.33332496881484985f);
+    p = fmaf(p, e, -0.4999997913837433f);
+    p = fmaf(p, e, 1.0f);
+    return p * e;
+}
+// max(x, 0) + log(1 + e^-|x|); a NaN stays one (fmaxf alone would drop it)
+__device__ __forceinline__ float softplus_f(float x) { return fmaxf(x, 0.f) + log1p_01(exp_neg(-fabsf(x))); }
+__device__ __forceinline__ float rcp_f(float x) {   // 1 / x, about 1 ulp
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// 1 / (1 + e^-x) from e^-|x|: both signs keep their relative accuracy
+__device__ __forceinline__ float sigmoid_f(float x) {
+    const float e = exp_neg(-fabsf(x));
+    const float r = rcp_f(1.f + e);
+    return x < 0.f ? e * r : r;
+}
+
+// ------------------------------------------------------------------ scan order
+// Token of scan position p, and its successors without divisions: inside a row (or column)
+// the token moves by `step`, at its end by `jump` more.
+struct Walk {
+    int n, i, inner, step, jump;
+    __device__ __forceinline__ Walk(int p, int H, int W, int dir) {
+        if (dir == GTR_L2R) {
+            n = p, i = 0, inner = 0x7fffffff, step = 1, jump = 0;
+        } else if (dir == GTR_R2L) {
+            const int y = p / W, r = p - y * W;
+            n = y * W + (W - 1 - r), i = r, inner = W, step = -1, jump = 2 * W;
+        } else {
+            const int x = p / H, r = p - x * H;
+            i = r, inner = H;
+            if (dir == GTR_T2B)
+                n = r * W + x, step = W, jump = 1 - H * W;
+            else
+                n = (H - 1 - r) * W + x, step = -W, jump = H * W + 1;
+        }
+    }
+    __device__ __forceinline__ void next() {
+        n += step;
+        if (++i == inner) {
+            i = 0;
+            n += jump;
+        }
+    }
+};
+__device__ __forceinline__ int token_of(int p, int H, int W, int dir) {
+    return dir == GTR_L2R ? p : Walk(p, H, W, dir).n;
+}
+
+// ------------------------------------------------------------------ host checks
+inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+inline bool aligned_to(const void *p, unsigned a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+struct Span {
+    const void *p;
+    long long bytes;
+};
+inline bool overlap(const Span &a, const Span &b) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+    return a.p && b.p && a.bytes > 0 && b.bytes > 0 && x < y + (uintptr_t)b.bytes && y < x + (uintptr_t)a.bytes;
+}
+// bytes from the first to behind the last element of `rows` rows of `cols` 16-bit elements, `ld` apart
+inline long long row_bytes(long long rows, long long ld, long long cols) {
+    return rows <= 0 ? 0 : ((rows - 1) * ld + cols) * 2;
+}
+constexpr long long kMaxTokens = (1LL << 30) - 1, kMaxElements = 1LL << 40;
+
+}  // namespace ops
+}  // namespace gtr

@@ -1,5 +1,6 @@
 """Python binding of the C ABI in include/gtr_gla.h, gtr_gla_bwd.h and gtr_swiglu.h
-(argument marshalling only).
+(argument marshalling only).  ``ssm`` and ``norm`` bind gtr_ssm.h and gtr_norm.h of the
+same library.
 
 Every step of the token mixer runs in the CUDA library ``libgtr_gla.so``; this
 module only checks tensor metadata, passes raw device pointers and the CUDA
@@ -25,7 +26,11 @@ STATIC_WS_BYTES = 4 << 20   # GTR_STATIC_WS_BYTES
 EXPORTED_SYMBOLS = ("gtr_gla_fwd", "gtr_gla_fwd_z", "gtr_gla_fwd_stack", "gtr_gla_init", "gtr_gla_workspace_bytes", "gtr_gla_fwd_ws",
                     "gtr_gla_fwd_static", "gtr_gla_device_status", "gtr_status_str", "gtr_gla_plan", "gtr_gla_version",
                     "gtr_gla_last_error", "gtr_gla_selftest_timeout", "gtr_spatial_swiglu_gate",
-                    "gtr_gla_bwd", "gtr_gla_bwd_workspace_bytes")
+                    "gtr_gla_bwd", "gtr_gla_bwd_workspace_bytes",
+                    "gtr_causal_conv_fwd", "gtr_causal_conv_bwd", "gtr_causal_conv_bwd_workspace_bytes",
+                    "gtr_ssm_scan_fwd", "gtr_ssm_scan_fwd_workspace_bytes", "gtr_ssm_scan_bwd",
+                    "gtr_ssm_scan_bwd_workspace_bytes", "gtr_group_norm_fwd", "gtr_group_norm_fwd_workspace_bytes",
+                    "gtr_group_norm_bwd", "gtr_group_norm_bwd_workspace_bytes")
 
 _lock = threading.Lock()
 _lib = None
@@ -77,6 +82,27 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         lib.gtr_gla_bwd.argtypes = [vp] * 7 + [i] * 8 + [vp] * 6 + [ctypes.c_size_t, vp]
         lib.gtr_gla_bwd_workspace_bytes.restype = ctypes.c_size_t
         lib.gtr_gla_bwd_workspace_bytes.argtypes = [i] * 7
+        sz, ll = ctypes.c_size_t, ctypes.c_longlong
+        lib.gtr_causal_conv_fwd.restype = i
+        lib.gtr_causal_conv_fwd.argtypes = [vp] * 4
+        lib.gtr_causal_conv_bwd_workspace_bytes.restype = sz
+        lib.gtr_causal_conv_bwd_workspace_bytes.argtypes = [i] * 5
+        lib.gtr_causal_conv_bwd.restype = i
+        lib.gtr_causal_conv_bwd.argtypes = [vp, vp, ll] + [vp] * 6 + [sz, vp]
+        for name in ("gtr_ssm_scan_fwd_workspace_bytes", "gtr_ssm_scan_bwd_workspace_bytes"):
+            getattr(lib, name).restype = sz
+            getattr(lib, name).argtypes = [i] * 5
+        lib.gtr_ssm_scan_fwd.restype = i
+        lib.gtr_ssm_scan_fwd.argtypes = [vp] * 4 + [sz, vp]
+        lib.gtr_ssm_scan_bwd.restype = i
+        lib.gtr_ssm_scan_bwd.argtypes = [vp, vp, ll] + [vp] * 3 + [sz, vp]
+        for name in ("gtr_group_norm_fwd_workspace_bytes", "gtr_group_norm_bwd_workspace_bytes"):
+            getattr(lib, name).restype = sz
+            getattr(lib, name).argtypes = [i] * 4
+        lib.gtr_group_norm_fwd.restype = i
+        lib.gtr_group_norm_fwd.argtypes = [vp] * 3 + [i] * 4 + [ctypes.c_float, i, i] + [vp] * 3 + [sz, vp]
+        lib.gtr_group_norm_bwd.restype = i
+        lib.gtr_group_norm_bwd.argtypes = [vp] * 5 + [i] * 6 + [vp] * 4 + [sz, vp]
         lib.gtr_gla_device_status.restype = i
         lib.gtr_gla_device_status.argtypes = [vp]
         lib.gtr_gla_init.restype = i
