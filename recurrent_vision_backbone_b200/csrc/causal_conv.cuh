@@ -40,6 +40,7 @@ __device__ __forceinline__ Raw<V> early_row(const Args &a, int b, int r, int K, 
 // channels, so a warp reads whole lines of each row whatever the scan order.
 template <typename T, int V, int K, int TP>
 __global__ void __launch_bounds__(kThreads) causal_conv_fwd_kernel(const Args a) {
+    chain_wait();
     const long long id = (long long)blockIdx.x * kThreads + threadIdx.x;
     const int g = (int)(id % a.groups);
     const long long t = id / a.groups;
@@ -118,6 +119,7 @@ constexpr int kLanes = 8, kAhead = 4;
 template <typename T, int V, int K>
 __global__ void __launch_bounds__(32 * kLanes) causal_conv_bwd_kernel(const Args a) {
     __shared__ float red[kLanes][32][V];
+    chain_wait();
     const int g = blockIdx.x % ((a.groups + 31) / 32) * 32 + threadIdx.x;
     const int part = blockIdx.x / ((a.groups + 31) / 32);
     const long long t = (long long)part * kLanes + threadIdx.y;
@@ -251,6 +253,7 @@ __global__ void __launch_bounds__(32 * kLanes) causal_conv_bwd_kernel(const Args
 template <int K>
 __global__ void __launch_bounds__(256) causal_conv_sum_kernel(const float *part, int parts, int D, float *gw, float *gb) {
     __shared__ float red[8][33];
+    chain_wait();
     const long long cols = (long long)(K + 1) * D, col = (long long)blockIdx.x * 32 + threadIdx.x;
     float s = 0.f;
     if (col < cols)

@@ -56,6 +56,7 @@ constexpr int kRowLanes = 8;
 template <typename T, int V, bool BWD>
 __global__ void __launch_bounds__(32 * kRowLanes) group_norm_sums_kernel(const Args a) {
     __shared__ float red[kRowLanes][32][V][2];
+    chain_wait();
     const int cb = blockIdx.x % a.cblocks, sb = blockIdx.x / a.cblocks;
     const int b = sb / a.splits, s = sb - b * a.splits;
     const int c = (cb * 32 + threadIdx.x) * V;
@@ -159,6 +160,7 @@ template <bool BWD>
 __global__ void __launch_bounds__(256) group_norm_groups_kernel(const Args a) {
     __shared__ float red[3][8];
     __shared__ float cols[2][8][33];
+    chain_wait();
     const float2 *part = reinterpret_cast<const float2 *>(a.part);
     const int tid = threadIdx.x;
     if ((long long)blockIdx.x < (long long)a.B * a.G) {
@@ -228,6 +230,7 @@ __global__ void __launch_bounds__(256) group_norm_groups_kernel(const Args a) {
 
 template <typename T, int V, bool BWD>
 __global__ void __launch_bounds__(32 * kRowLanes) group_norm_apply_kernel(const Args a) {
+    chain_wait();
     const int cb = blockIdx.x % a.cblocks, sb = blockIdx.x / a.cblocks;
     const int b = sb / a.splits, s = sb - b * a.splits;
     const int c = (cb * 32 + threadIdx.x) * V;
@@ -315,10 +318,10 @@ static cudaError_t norm_launch(gn::Args a, cudaStream_t s) {
     const long long groups = (long long)a.B * a.G + (BWD && (a.gg || a.gb) ? (a.C + 31) / 32 : 0);
     if (blocks > 0x7fffffffLL || groups > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     const dim3 thr(32, gn::kRowLanes);
-    gn::group_norm_sums_kernel<T, V, BWD><<<(unsigned)blocks, thr, 0, s>>>(a);
-    gn::group_norm_groups_kernel<BWD><<<(unsigned)groups, 256, 0, s>>>(a);
-    gn::group_norm_apply_kernel<T, V, BWD><<<(unsigned)blocks, thr, 0, s>>>(a);
-    return cudaGetLastError();
+    cudaError_t e = launch_after(gn::group_norm_sums_kernel<T, V, BWD>, (unsigned)blocks, thr, 0, s, a);
+    if (e == cudaSuccess) e = launch_after(gn::group_norm_groups_kernel<BWD>, (unsigned)groups, dim3(256), 0, s, a);
+    if (e == cudaSuccess) e = launch_after(gn::group_norm_apply_kernel<T, V, BWD>, (unsigned)blocks, thr, 0, s, a);
+    return e;
 }
 template <bool BWD>
 static cudaError_t norm_dispatch(const gn::Args &a, int dtype, cudaStream_t s) {

@@ -47,6 +47,10 @@ struct Elem<__half> {
     // whether a result left the type's range (|f| above the largest fp16, or NaN); the
     // running maximum of |f| is what is tested, which fmaxf would lose a NaN from
     static __device__ __forceinline__ bool bad(float f) { return !(fabsf(f) <= 65504.f); }
+    // the same of rounded values, two to a word (or one): an exponent of all ones
+    static __device__ __forceinline__ bool bad_raw(uint32_t w) {
+        return (w & 0x7c00u) == 0x7c00u || (w & 0x7c000000u) == 0x7c000000u;
+    }
 };
 template <>
 struct Elem<__nv_bfloat16> {
@@ -60,6 +64,7 @@ struct Elem<__nv_bfloat16> {
         return *reinterpret_cast<const uint32_t *>(&h);
     }
     static __device__ __forceinline__ bool bad(float) { return false; }   // bf16 holds what float32 holds
+    static __device__ __forceinline__ bool bad_raw(uint32_t) { return false; }
 };
 
 // V consecutive elements as raw words: V = 8 is one 16-byte access, 4 an 8-byte one, 2 a
@@ -83,6 +88,12 @@ __device__ __forceinline__ Raw<V> load_raw(const uint16_t *p) {
         r.w[0] = __ldg(p);
     }
     return r;
+}
+template <int V>
+__device__ __forceinline__ Raw<V> load_raw_shared(const uint16_t *p) {
+    static_assert(V == 8, "16-byte pieces");
+    const uint4 x = *reinterpret_cast<const uint4 *>(p);
+    return {{x.x, x.y, x.z, x.w}};
 }
 template <int V>
 __device__ __forceinline__ void store_raw(uint16_t *p, const Raw<V> &r) {
@@ -127,6 +138,20 @@ __device__ __forceinline__ Raw<V> pack(const float (&f)[V]) {
     return r;
 }
 
+// ------------------------------------------------------------------ asynchronous copies
+// 16 bytes to shared memory; `bytes` of them (0 or 16) are read, the rest becomes zeros.
+__device__ __forceinline__ void copy16_async(void *dst, const void *src, uint32_t bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                     static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
+                 "l"(src), "r"(bytes)
+                 : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>   // waits until at most N of this thread's groups are in flight
+__device__ __forceinline__ void copy_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 // ------------------------------------------------------------------ functions
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -135,13 +160,6 @@ __device__ __forceinline__ float ex2(float x) {   // 2^x, about 2 ulp; 0 below 2
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
-}
-// e^x for x <= 0 with x log2(e) kept in two parts, so that a large |x| costs no accuracy
-__device__ __forceinline__ float exp_neg(float x) {
-    const float t = x * kLog2e;
-    const float lo = fmaf(x, kLog2e, -t) + x * 1.925963033e-8f;   // log2(e) - its float32 value
-    const float e = ex2(t);
-    return t < -126.f ? e : fmaf(e * kLn2, lo, e);
 }
 // log(1 + e) for e in [0, 1]: e times a polynomial of degree 10, interpolating log(1 + e) / e at
 // Chebyshev nodes (relative error 8.5e-10; 1.2e-7 evaluated in float32)
@@ -159,18 +177,46 @@ __device__ __forceinline__ float log1p_01(float e) {
     p = fmaf(p, e, 1.0f);
     return p * e;
 }
-// max(x, 0) + log(1 + e^-|x|); a NaN stays one (fmaxf alone would drop it)
-__device__ __forceinline__ float softplus_f(float x) { return fmaxf(x, 0.f) + log1p_01(exp_neg(-fabsf(x))); }
-__device__ __forceinline__ float rcp_f(float x) {   // 1 / x, about 1 ulp
+// max(x, 0) + log(1 + e^-|x|) of two values at once (packed arithmetic: half the instructions);
+// relative error about |x| 2^-24 from the exponent's rounding, and a NaN stays one (fmaxf alone
+// would drop it)
+__device__ __forceinline__ float2 splat(float x) { return make_float2(x, x); }
+__device__ __forceinline__ float2 softplus_2(float2 x, float2 &e) {   // e: e^-|x|
+    e = make_float2(ex2(fabsf(x.x) * -kLog2e), ex2(fabsf(x.y) * -kLog2e));
+    float2 p = splat(0.001986696617677808f);   // log1p_01, twice
+    p = __ffma2_rn(p, e, splat(-0.013187826611101627f));
+    p = __ffma2_rn(p, e, splat(0.04100657254457474f));
+    p = __ffma2_rn(p, e, splat(-0.08188040554523468f));
+    p = __ffma2_rn(p, e, splat(0.12377995967997313f));
+    p = __ffma2_rn(p, e, splat(-0.16087622940540314f));
+    p = __ffma2_rn(p, e, splat(0.19885820150375366f));
+    p = __ffma2_rn(p, e, splat(-0.24986496567726135f));
+    p = __ffma2_rn(p, e, splat(0.33332496881484985f));
+    p = __ffma2_rn(p, e, splat(-0.4999997913837433f));
+    p = __ffma2_rn(p, e, splat(1.0f));
+    return __ffma2_rn(p, e, make_float2(fmaxf(x.x, 0.f), fmaxf(x.y, 0.f)));
+}
+__device__ __forceinline__ float rcp_f(float x) {   // 1 / x, about 1 ulp; 0 for infinities
     float y;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-// 1 / (1 + e^-x) from e^-|x|: both signs keep their relative accuracy
-__device__ __forceinline__ float sigmoid_f(float x) {
-    const float e = exp_neg(-fabsf(x));
+__device__ __forceinline__ float sigmoid_f(float x) { return rcp_f(1.f + ex2(x * -kLog2e)); }
+// sigmoid(x), softplus's derivative, from e = e^-|x|: relative accuracy for either sign
+__device__ __forceinline__ float sigmoid_of(float x, float e) {
     const float r = rcp_f(1.f + e);
     return x < 0.f ? e * r : r;
+}
+__device__ __forceinline__ float softplus_f(float x) {
+    return fmaxf(x, 0.f) + log1p_01(ex2(fabsf(x) * -kLog2e));
+}
+
+// ------------------------------------------------------------------ launches in a chain
+// A kernel launched with launch_after may start while the one ahead of it in the stream drains;
+// it waits here, before its first access to global memory, until that one has finished.
+__device__ __forceinline__ void chain_wait() {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
 // ------------------------------------------------------------------ scan order
@@ -200,6 +246,14 @@ struct Walk {
             n += jump;
         }
     }
+    __device__ __forceinline__ void advance(int k) {
+        n += k * step;
+        i += k;
+        while (i >= inner) {
+            i -= inner;
+            n += jump;
+        }
+    }
 };
 __device__ __forceinline__ int token_of(int p, int H, int W, int dir) {
     return dir == GTR_L2R ? p : Walk(p, H, W, dir).n;
@@ -208,6 +262,22 @@ __device__ __forceinline__ int token_of(int p, int H, int W, int dir) {
 // ------------------------------------------------------------------ host checks
 inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 inline bool aligned_to(const void *p, unsigned a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+// Launches a kernel of one Args argument (and perhaps an int) that begins with chain_wait().
+template <typename K, typename... A>
+inline cudaError_t launch_after(K kernel, unsigned grid, dim3 block, size_t smem, cudaStream_t stream, A... args) {
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute attr[1];
+    cfg.gridDim = dim3(grid, 1, 1);
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
 
 struct Span {
     const void *p;

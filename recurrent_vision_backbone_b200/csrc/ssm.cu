@@ -117,8 +117,7 @@ static cudaError_t conv_fwd_launch(cv::Args a, cudaStream_t s) {
     a.tiles = (a.N + TP - 1) / TP;
     const long long blocks = ((long long)a.B * a.tiles * a.groups + cv::kThreads - 1) / cv::kThreads;
     if (blocks > kMaxGrid) return cudaErrorInvalidConfiguration;
-    cv::causal_conv_fwd_kernel<T, V, K, TP><<<(unsigned)blocks, cv::kThreads, 0, s>>>(a);
-    return cudaGetLastError();
+    return launch_after(cv::causal_conv_fwd_kernel<T, V, K, TP>, (unsigned)blocks, dim3(cv::kThreads), 0, s, a);
 }
 template <typename T, int V>
 static cudaError_t conv_fwd_k(const cv::Args &a, int K, cudaStream_t s) {
@@ -134,10 +133,11 @@ static cudaError_t conv_bwd_launch(cv::Args a, const ConvPlan &p, float *gw, flo
     a.groups = (a.D + V - 1) / V;
     const long long blocks = p.parts * ((a.groups + 31) / 32);
     if (blocks > kMaxGrid) return cudaErrorInvalidConfiguration;
-    cv::causal_conv_bwd_kernel<T, V, K><<<(unsigned)blocks, dim3(32, cv::kLanes), 0, s>>>(a);
+    const cudaError_t e = launch_after(cv::causal_conv_bwd_kernel<T, V, K>, (unsigned)blocks, dim3(32, cv::kLanes), 0, s, a);
+    if (e != cudaSuccess) return e;
     const long long cols = (long long)(K + 1) * a.D;
-    cv::causal_conv_sum_kernel<K><<<(unsigned)((cols + 31) / 32), dim3(32, 8), 0, s>>>(a.part, (int)p.parts, a.D, gw, gb);
-    return cudaGetLastError();
+    return launch_after(cv::causal_conv_sum_kernel<K>, (unsigned)((cols + 31) / 32), dim3(32, 8), 0, s,
+                        (const float *)a.part, (int)p.parts, a.D, gw, gb);
 }
 template <typename T, int V>
 static cudaError_t conv_bwd_k(const cv::Args &a, int K, const ConvPlan &p, float *gw, float *gb, cudaStream_t s) {
@@ -162,17 +162,24 @@ static int state_pad(int S) { return S <= 8 ? 8 : S <= 16 ? 16 : 32; }
 
 struct ScanPlan {
     int P, L;
+    int SL;   // lanes that share a channel in the walk that writes the outputs
 };
+// The walks of a forward scan.  With 96 blocks of 128 channels or more, one walk over whole
+// sequences: two lanes a channel until the channels alone are three warps a scheduler, then one (8 x 2304
+// tokens of 2048 channels, 128 blocks: 306 us with two lanes, 425 with one, 384 with four; 397 in four
+// chunks).  Below that, as many chunks as make one wave of four blocks an SM, at least 32 tokens each
+// (16384 tokens of 1024 channels, 8 blocks: 182 us with 74 chunks, 201 with 92, 250 with 37).
 static ScanPlan scan_fwd_plan(int B, long long N, int D) {
     const long long base = (long long)B * ((D + sc::kThreads - 1) / sc::kThreads);
-    long long P = base * 2 > kSmAim ? 1 : (kSmAim + base - 1) / base;
+    const long long P = base >= 96 ? 1 : kSmAim / base;
     long long L = (N + P - 1) / P;
-    L = (L + sc::kTok - 1) / sc::kTok * sc::kTok;
+    L = (L + 7) / 8 * 8;
     if (L < 32) L = 32;
     if (L > N) L = N;
     ScanPlan r{};
     r.L = (int)L;
     r.P = (int)((N + L - 1) / L);
+    r.SL = r.P == 1 && base < 148 * 3 ? 2 : 1;
     return r;
 }
 static size_t scan_fwd_bytes(int B, int D, int S, const ScanPlan &p) {
@@ -187,8 +194,8 @@ static int grad_tile(int S) {
 }
 static ScanPlan scan_bwd_plan(int B, long long N, int D, int S) {
     const long long base = (long long)B * ((D + grad_tile(S) - 1) / grad_tile(S));
-    int L = sc::kMaxChunkBwd;
-    while (L > 16 && base * ((N + L - 1) / L) < kSmAim) L /= 2;
+    // shorter chunks where whole ones would not fill the machine (three blocks an SM) twice
+    const int L = base * ((N + sc::kMaxChunkBwd - 1) / sc::kMaxChunkBwd) < 148 * 3 * 2 ? 32 : sc::kMaxChunkBwd;
     ScanPlan r{};
     r.L = L;
     r.P = (int)((N + L - 1) / L);
@@ -266,24 +273,44 @@ static int ssm_inputs(const gtr_ssm_t *m, const sc::Args &a, Span *s) {
     return n;
 }
 
-template <typename T, int NS>
-static cudaError_t scan_fwd_launch(const sc::Args &a, cudaStream_t s) {
-    if (a.P > 1) {
-        sc::ssm_walk_kernel<T, NS, sc::kLocal><<<(unsigned)((long long)a.tiles * a.B * (a.P - 1)), sc::kThreads, 0, s>>>(a);
-        const long long n = (long long)a.B * a.D * 2 * NS;
-        sc::ssm_fold_kernel<2 * NS, false><<<(unsigned)((n + 255) / 256), 256, 0, s>>>(a);
+template <typename T, int SP, int MODE, int SL>
+static cudaError_t walk_launch(const sc::Args &a, bool wide, cudaStream_t s) {
+    const unsigned grid = (unsigned)((long long)a.tiles * a.B * (MODE == sc::kLocal ? a.P - 1 : a.P));
+    const auto kernel = wide ? sc::ssm_walk_kernel<T, SP, MODE, true, SL> : sc::ssm_walk_kernel<T, SP, MODE, false, SL>;
+    // A walk that opens a call and covers many SMs starts plainly: blocks that wait on SMs where the
+    // call ahead happens to have left room end up unevenly spread (468 us for 428 at 8 x 2304 tokens of
+    // 2048 channels)
+    if ((MODE != sc::kOut || a.P == 1) && grid > 148) {
+        kernel<<<grid, sc::kThreads, 0, s>>>(a);
+        return cudaGetLastError();
     }
-    sc::ssm_walk_kernel<T, NS, sc::kOut><<<(unsigned)((long long)a.tiles * a.B * a.P), sc::kThreads, 0, s>>>(a);
-    return cudaGetLastError();
+    return launch_after(kernel, grid, dim3(sc::kThreads), 0, s, a);
+}
+template <int SP, bool BWD>
+static cudaError_t fold_launch(const sc::Args &a, cudaStream_t s) {
+    const long long n = (long long)a.B * a.D * SP * (BWD ? 2 : 1);
+    return launch_after(sc::ssm_fold_kernel<SP, BWD>, (unsigned)((n + sc::kFoldThreads - 1) / sc::kFoldThreads),
+                        dim3(sc::kFoldThreads), 0, s, a);
+}
+template <typename T, int SP>
+static cudaError_t scan_fwd_launch(const sc::Args &a, int sl, bool wide, cudaStream_t s) {
+    cudaError_t e = cudaSuccess;
+    if (a.P > 1) {
+        e = walk_launch<T, SP, sc::kLocal, 1>(a, wide, s);
+        if (e == cudaSuccess) e = fold_launch<SP, false>(a, s);
+    }
+    if (e != cudaSuccess) return e;
+    sc::Args o = a;
+    o.tiles = (a.D * (long long)sl + sc::kThreads - 1) / sc::kThreads;
+    return sl == 1 ? walk_launch<T, SP, sc::kOut, 1>(o, wide, s) : walk_launch<T, SP, sc::kOut, 2>(o, wide, s);
 }
 template <typename T, int S>
 static cudaError_t token_launch(const sc::Args &a, cudaStream_t s) {
     const long long n = (long long)a.B * a.D * (S / 4);
-    sc::ssm_token_kernel<T, S><<<(unsigned)((n + 255) / 256), 256, 0, s>>>(a);
-    return cudaGetLastError();
+    return launch_after(sc::ssm_token_kernel<T, S>, (unsigned)((n + 255) / 256), dim3(256), 0, s, a);
 }
 template <typename T>
-static cudaError_t scan_fwd_dispatch(const sc::Args &a, cudaStream_t s) {
+static cudaError_t scan_fwd_dispatch(const sc::Args &a, int sl, bool wide, cudaStream_t s) {
     // one token: lanes along the states; other numbers of states take the walk
     if (a.N == 1) {
         switch (a.S) {
@@ -294,43 +321,43 @@ static cudaError_t scan_fwd_dispatch(const sc::Args &a, cudaStream_t s) {
         }
     }
     switch (state_pad(a.S)) {
-    case 8: return scan_fwd_launch<T, 4>(a, s);
-    case 16: return scan_fwd_launch<T, 8>(a, s);
-    default: return scan_fwd_launch<T, 16>(a, s);
+    case 8: return scan_fwd_launch<T, 8>(a, sl, wide, s);
+    case 16: return scan_fwd_launch<T, 16>(a, sl, wide, s);
+    default: return scan_fwd_launch<T, 32>(a, sl, wide, s);
     }
 }
 
 template <typename T, int SP>
-static cudaError_t scan_bwd_launch(sc::Args a, cudaStream_t s) {
+static cudaError_t scan_bwd_launch(sc::Args a, bool wide, cudaStream_t s) {
     using Lay = sc::GradLayout<SP>;
-    if (a.P > 1) {
-        a.tiles = (a.D + sc::kThreads - 1) / sc::kThreads;
-        sc::ssm_walk_kernel<T, SP / 2, sc::kLocalBwd><<<(unsigned)((long long)a.tiles * a.B * a.P), sc::kThreads, 0, s>>>(a);
-        const long long n = (long long)a.B * a.D * SP;
-        sc::ssm_fold_kernel<SP, true><<<(unsigned)((n + 255) / 256), 256, 0, s>>>(a);
-    }
-    a.tiles = (a.D + Lay::CT - 1) / Lay::CT;
     const size_t smem = (size_t)Lay::floats(a.L) * sizeof(float);
-    cudaError_t e = cudaFuncSetAttribute(sc::ssm_grad_kernel<T, SP>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    const auto grad = a.pairs ? sc::ssm_grad_kernel<T, SP, true> : sc::ssm_grad_kernel<T, SP, false>;
+    cudaError_t e = cudaFuncSetAttribute(grad, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e == cudaSuccess && a.P > 1) {
+        a.tiles = (a.D + sc::kThreads - 1) / sc::kThreads;
+        e = walk_launch<T, SP, sc::kLocalBwd, 1>(a, wide, s);
+        if (e == cudaSuccess) e = fold_launch<SP, true>(a, s);
+    }
     if (e != cudaSuccess) return e;
-    sc::ssm_grad_kernel<T, SP><<<(unsigned)((long long)a.tiles * a.B * a.P), sc::kThreads, smem, s>>>(a);
+    a.tiles = (a.D + Lay::CT - 1) / Lay::CT;
+    e = launch_after(grad, (unsigned)((long long)a.tiles * a.B * a.P), dim3(sc::kThreads), smem, s, a);
+    if (e != cudaSuccess) return e;
     const long long bc = ((long long)a.B * a.N * 2 * SP + 255) / 256, rest = ((long long)a.D * (SP + 2) + 31) / 32;
-    sc::ssm_grad_sum_kernel<T, SP><<<(unsigned)(bc + rest), 256, 0, s>>>(a, (int)bc);
-    return cudaGetLastError();
+    return launch_after(sc::ssm_grad_sum_kernel<T, SP>, (unsigned)(bc + rest), dim3(256), 0, s, a, (int)bc);
 }
 template <typename T>
-static cudaError_t scan_bwd_dispatch(const sc::Args &a, cudaStream_t s) {
+static cudaError_t scan_bwd_dispatch(const sc::Args &a, bool wide, cudaStream_t s) {
     switch (state_pad(a.S)) {
-    case 8: return scan_bwd_launch<T, 8>(a, s);
-    case 16: return scan_bwd_launch<T, 16>(a, s);
-    default: return scan_bwd_launch<T, 32>(a, s);
+    case 8: return scan_bwd_launch<T, 8>(a, wide, s);
+    case 16: return scan_bwd_launch<T, 16>(a, wide, s);
+    default: return scan_bwd_launch<T, 32>(a, wide, s);
     }
 }
 
 // Whether the launches of a scan fit a grid (blocks along x only).
 static bool grid_too_large(int B, long long N, int D, int S, long long P) {
     const long long sp = state_pad(S), tiles = (D + 31) / 32;
-    return (long long)B * P > kMaxGrid || (long long)B * P * tiles > kMaxGrid || (long long)B * D > kMaxGrid * 256 / sp ||
+    return (long long)B * P > kMaxGrid || (long long)B * P * tiles > kMaxGrid || (long long)B * D > kMaxGrid * (sc::kFoldThreads / 2) / sp ||
            (long long)B * N > kMaxGrid * 8 / sp - (D * (sp + 2) + 31) / 32;
 }
 
@@ -456,7 +483,11 @@ extern "C" gtr_status_t gtr_ssm_scan_fwd(const gtr_ssm_t *ssm, void *out, float 
     a.tiles = (a.D + sc::kThreads - 1) / sc::kThreads;
     a.hs = static_cast<float *>(workspace);
     a.sdt = a.hs + align256((size_t)a.B * a.P * a.D * state_pad(a.S) * sizeof(float)) / sizeof(float);
-    return ops_cuda_status(ssm->dtype == GTR_F16 ? scan_fwd_dispatch<__half>(a, s) : scan_fwd_dispatch<__nv_bfloat16>(a, s));
+    const void *ps[] = {a.u, a.dt, a.z};
+    const long long lds[] = {a.ldu, a.lddt, a.z ? a.ldz : 0};
+    const bool wide = rows_on(16, a.D, ps, 3, lds, 3);
+    return ops_cuda_status(ssm->dtype == GTR_F16 ? scan_fwd_dispatch<__half>(a, p.SL, wide, s)
+                                                 : scan_fwd_dispatch<__nv_bfloat16>(a, p.SL, wide, s));
 }
 
 extern "C" size_t gtr_ssm_scan_bwd_workspace_bytes(int B, int Hgrid, int Wgrid, int D, int S) {
@@ -525,5 +556,11 @@ extern "C" gtr_status_t gtr_ssm_scan_bwd(const gtr_ssm_t *ssm, const void *d_out
     a.pbc = reinterpret_cast<float *>(ws + w.pbc);
     a.pd = reinterpret_cast<float *>(ws + w.pd);
     a.pt = reinterpret_cast<float *>(ws + w.pt);
-    return ops_cuda_status(ssm->dtype == GTR_F16 ? scan_bwd_dispatch<__half>(a, s) : scan_bwd_dispatch<__nv_bfloat16>(a, s));
+    const void *ps[] = {a.u, a.dt, a.z, a.dy};
+    const long long lds[] = {a.ldu, a.lddt, a.z ? a.ldz : 0, a.lddy};
+    const bool wide = rows_on(16, a.D, ps, 4, lds, 4);
+    const void *po[] = {a.du, a.ddt, a.dz};
+    a.pairs = rows_on(4, a.D, ps, 4, lds, 4) && rows_on(4, a.D, po, 3, lds, 0);
+    return ops_cuda_status(ssm->dtype == GTR_F16 ? scan_bwd_dispatch<__half>(a, wide, s)
+                                                 : scan_bwd_dispatch<__nv_bfloat16>(a, wide, s));
 }

@@ -18,20 +18,21 @@
 // The walk of step 1 costs as much as step 3, so P is 1 (step 3 alone) as soon as the channels
 // alone keep the schedulers busy; else just large enough to do so.
 //
-// Walk layout: two neighbouring lanes share two neighbouring channels, each lane holding half
-// of the states of both (NS states of its own channel and of its neighbour's).  A lane loads its
-// own channel only; the time step and the input are exchanged by one shuffle each, the partial
-// sums of y by another, and a warp reads 64 consecutive bytes of every row.  B and C of a tile of
-// kTok tokens are staged in shared memory as float32 and read as broadcasts, each value serving
-// two channels.  The next tile's rows are requested before a tile is computed.
+// Walk layout: a lane is a channel and holds all its states, a block 128 neighbouring channels.
+// Tiles of kTok tokens pass through shared memory: the channels' rows as 16-byte asynchronous
+// copies, kStages tiles deep (or element by element where rows do not line up to 16 bytes), B and C
+// as float32, read as broadcasts.  The time steps of two tokens are formed at once (packed
+// arithmetic), and so are two states of a token.
 #pragma once
+
+#include <type_traits>
 
 namespace gtr {
 namespace sc {
 
 using namespace ops;
 
-constexpr int kThreads = 128, kTok = 8;
+constexpr int kThreads = 128, kStages = 3;
 
 struct Args {
     const uint16_t *u, *dt, *bm, *cm, *z, *dy;
@@ -41,6 +42,7 @@ struct Args {
     long long ldu, lddt, ldb, ldc, ldz, lddy;
     int B, H, W, N, D, S, dir, softplus;
     int P, L, tiles;                // chunks a sequence, tokens a chunk, channel tiles
+    int pairs;                      // backward: rows of channels start on 4 bytes and are even
     float *hs, *gs, *sdt;           // workspace: [B][P][D][SP], the same, [B][P][D]
     // backward
     uint16_t *du, *ddt, *dz, *dB, *dC;
@@ -48,34 +50,139 @@ struct Args {
     float *pbc, *pd, *pt;           // workspace: [tiles][B N][2 SP], [B P][D], [B P][D]
 };
 
-__device__ __forceinline__ float2 f2(float x) { return make_float2(x, x); }
 __device__ __forceinline__ uint16_t ld16(const uint16_t *p, bool in) { return in ? __ldg(p) : (uint16_t)0; }
 
 enum { kLocal = 0, kOut = 1, kLocalBwd = 2 };
 
+// Sums over lanes whose index differs in the bits [LO, HI): v[0 .. NV - 1] of every lane.  While
+// a lane holds several values a round exchanges half of them; then whole values.  Lane l ends
+// with the sums of the values [idx, idx + left) in v[0 .. left - 1], where idx is returned.
+template <int LO, int HI, int NV>
+__device__ __forceinline__ int butterfly(float *v, int lane) {
+    if constexpr (LO >= HI) {
+        return 0;
+    } else if constexpr (NV > 1) {
+        const bool up = lane & LO;
+#pragma unroll
+        for (int i = 0; i < NV / 2; ++i) {
+            const float send = up ? v[i] : v[i + NV / 2], keep = up ? v[i + NV / 2] : v[i];
+            v[i] = keep + __shfl_xor_sync(0xffffffffu, send, LO);
+        }
+        return (up ? NV / 2 : 0) + butterfly<LO * 2, HI, NV / 2>(v, lane);
+    } else {
+        v[0] += __shfl_xor_sync(0xffffffffu, v[0], LO);
+        return butterfly<LO * 2, HI, 1>(v, lane);
+    }
+}
+__host__ __device__ constexpr int left_of(int nv, int lanes) { return nv > lanes ? nv / lanes : 1; }
+
+// Rows of one tensor that a walk stages: the thread's 8 channels of its token.
+template <bool WIDE>
+__device__ __forceinline__ void stage_row(uint16_t *dst, const uint16_t *src, bool in, int left) {
+    if constexpr (WIDE) {
+        copy16_async(dst, src, in && left > 0 ? 16u : 0u);   // 0 bytes: zeros
+    } else {
+        Raw<8> r;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            r.w[i] = (uint32_t)ld16(src + 2 * i, in && 2 * i < left) | (uint32_t)ld16(src + 2 * i + 1, in && 2 * i + 1 < left) << 16;
+        store_raw<8>(dst, r);
+    }
+}
+
+template <int MODE>
+__host__ __device__ constexpr int walk_rows() { return MODE == kLocal ? 2 : MODE == kOut ? 3 : 4; }
+// Blocks an SM that a walk's registers allow: four where the plan counts on them; two lanes a channel
+// run when the channels alone are few blocks an SM.
+template <int SP, int MODE, int SL>
+__host__ __device__ constexpr int walk_blocks() { return SP > 16 ? 1 : MODE == kLocalBwd ? 3 : SL > 1 ? 2 : 4; }
+
 // One walk over one chunk.  kLocal: hs[b][j] = the state reached from zero, sdt = the sum of the
-// time steps.  kLocalBwd: also gs[b][j] = sum_p (prod_{r <= p} a_r) C_p dy_p, the gradient that
+// time steps.  kLocalBwd: also gs[b][j] = sum_p (prod_{r <= p} a_r) C_p e_p, the gradient that
 // the chunk's outputs send to the state entering it.  kOut: outputs and the final state.
-template <typename T, int NS, int MODE>
-__global__ void __launch_bounds__(kThreads) ssm_walk_kernel(const Args a) {
-    constexpr int SP = 2 * NS;                  // states, padded with zero B and C
-    constexpr int kStage = kTok * SP * 2 / kThreads;   // B and C values a thread stages per tile
-    static_assert(kStage >= 1, "a tile of B and C has at least one value a thread");
-    __shared__ __align__(16) float bc[2][2][kTok][SP];
-    const int tid = threadIdx.x, lane = tid & 31, sl = lane & 1;
+template <typename T, int SP, int MODE, bool WIDE, int SL>
+__global__ void __launch_bounds__(kThreads, walk_blocks<SP, MODE, SL>()) ssm_walk_kernel(const Args a) {
+    static_assert(SL == 1 || (SL == 2 && MODE == kOut), "the local walks have chunks enough");
+    constexpr int CH = kThreads / SL;           // channels of the block
+    constexpr int TOK = 8 * SL;                 // tokens of a tile
+    constexpr int NP = SP / SL / 2;             // pairs of states of a lane
+    constexpr int R = walk_rows<MODE>();        // u, dt, z, dy
+    constexpr int RT = 16 / SL;                 // threads that stage a token's row
+    constexpr int NBC = 2 * SP / RT;            // B and C values a thread stages per tile
+    __shared__ __align__(16) uint16_t rows[kStages][R][TOK][CH];
+    __shared__ __align__(16) float bc[2][2][TOK][SP];
+    __shared__ __align__(16) uint16_t outs[2][MODE == kOut ? TOK : 1][MODE == kOut ? CH : 8];
+    chain_wait();
+    const int tid = threadIdx.x;
     const int ct = blockIdx.x % a.tiles;
     const int cj = blockIdx.x / a.tiles;
     const int nj = MODE == kLocal ? a.P - 1 : a.P;   // the last chunk's reached state is not needed
     const int b = cj / nj, j = cj - b * nj;
     const int p0 = j * a.L, p1 = min(a.N, p0 + a.L);
-    const int c = ct * kThreads + tid, co = c ^ 1, n0 = sl * NS;
-    const bool cv = c < a.D, cov = co < a.D;
+    const int sl = tid % SL, cl = tid / SL, n0 = sl * 2 * NP;   // lane of the channel, channel, first state
+    const int c = ct * CH + cl;
+    const bool cv = c < a.D;
     const long long row0 = (long long)b * a.N;
+    const bool gate = a.z != nullptr && MODE != kLocal, sp_on = a.softplus != 0;
 
-    float2 Ao[NS / 2], Ax[NS / 2], ho[NS / 2], hx[NS / 2];   // own channel, exchanged channel
-    float2 po[NS / 2], px[NS / 2], go[NS / 2], gx[NS / 2];   // kLocalBwd only
+    // staging: this thread's token of a tile, 8 of its channels, and some of its B and C
+    const int tt = tid / RT, tc = tid % RT;
+    const int c8 = ct * CH + tc * 8, left = a.D - c8;
+    Walk wk(min(p0 + tt, a.N - 1), a.H, a.W, a.dir);
+    uint16_t rb[NBC];
+    auto stage = [&](int pb, int s) {   // request the rows of the tile at pb
+        const bool in = pb + tt < p1;
+        const long long row = row0 + (in ? wk.n : 0);
+        stage_row<WIDE>(&rows[s][0][tt][tc * 8], a.u + row * a.ldu + c8, in, left);
+        stage_row<WIDE>(&rows[s][1][tt][tc * 8], a.dt + row * a.lddt + c8, in, left);
+        if (MODE != kLocal && gate) stage_row<WIDE>(&rows[s][MODE != kLocal ? 2 : 0][tt][tc * 8], a.z + row * a.ldz + c8, in, left);
+        if (MODE == kLocalBwd) stage_row<WIDE>(&rows[s][MODE == kLocalBwd ? 3 : 0][tt][tc * 8], a.dy + row * a.lddy + c8, in, left);
+        if (WIDE) copy_commit();
+    };
+    // values v = tc + RT i of a token's [B ; C]
+    auto load_bc = [&](int pb, int n) {
+        const bool in = pb + tt < p1;
+        const long long row = row0 + (in ? n : 0);
+#pragma unroll
+        for (int i = 0; i < NBC; ++i) {
+            const int v = tc + RT * i, k = v % SP;
+            const bool isc = v >= SP;
+            rb[i] = isc ? ld16(a.cm + row * a.ldc + k, in && k < a.S && MODE != kLocal) : ld16(a.bm + row * a.ldb + k, in && k < a.S);
+        }
+    };
+    // the token of this thread in this tile and the next: rows are asked for kStages - 1 tiles
+    // ahead, B and C one tile ahead
+    int tok[kStages - 1];
+#pragma unroll
+    for (int s = 0; s < kStages - 1; ++s) {
+        tok[s] = wk.n;
+        stage(p0 + s * TOK, s);
+        wk.advance(TOK);
+    }
+    load_bc(p0, tok[0]);
+    // the outputs of a tile pass through shared memory, so that they leave as rows
+    bool bad = false;
+    auto flush = [&](int pb, int n, int buf) {
+        if (pb + tt >= p1 || left <= 0) return;
+        const Raw<8> r = load_raw_shared<8>(&outs[buf][MODE == kOut ? tt : 0][MODE == kOut ? tc * 8 : 0]);
+        uint16_t *dst = a.out + (row0 + n) * a.D + c8;
+        if (WIDE) {   // whole pieces
+            bad |= Elem<T>::bad_raw(r.w[0]) | Elem<T>::bad_raw(r.w[1]) | Elem<T>::bad_raw(r.w[2]) | Elem<T>::bad_raw(r.w[3]);
+            store_raw<8>(dst, r);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (i < left) {
+                    const uint16_t v = (uint16_t)(i & 1 ? r.w[i / 2] >> 16 : r.w[i / 2]);
+                    bad |= Elem<T>::bad_raw(v);
+                    dst[i] = v;
+                }
+        }
+    };
+
+    float2 A2[NP], h[NP], pr[NP], g[NP];   // pr, g: kLocalBwd
     const float *hin = nullptr;
-    long long hstride = SP;
+    int hstride = SP;
     if (MODE == kOut) {
         if (j == 0) {
             // with several chunks the fold's copy of init_state: the last chunk may already have
@@ -88,189 +195,201 @@ __global__ void __launch_bounds__(kThreads) ssm_walk_kernel(const Args a) {
         }
     }
 #pragma unroll
-    for (int k = 0; k < NS; ++k) {
-        const int n = n0 + k;
-        const bool in = n < a.S;
-        float *A1 = k & 1 ? &Ao[k / 2].y : &Ao[k / 2].x, *A2 = k & 1 ? &Ax[k / 2].y : &Ax[k / 2].x;
-        float *h1 = k & 1 ? &ho[k / 2].y : &ho[k / 2].x, *h2 = k & 1 ? &hx[k / 2].y : &hx[k / 2].x;
-        *A1 = in && cv ? __ldg(a.A + (long long)c * a.S + n) * kLog2e : 0.f;
-        *A2 = in && cov ? __ldg(a.A + (long long)co * a.S + n) * kLog2e : 0.f;
-        *h1 = hin != nullptr && in && cv ? hin[(long long)c * hstride + n] : 0.f;
-        *h2 = hin != nullptr && in && cov ? hin[(long long)co * hstride + n] : 0.f;
+    for (int k = 0; k < 2 * NP; ++k) {
+        const bool in = n0 + k < a.S && cv;
+        const float av = in ? __ldg(a.A + (long long)c * a.S + n0 + k) * kLog2e : 0.f;
+        const float hv = hin != nullptr && in ? hin[(long long)c * hstride + n0 + k] : 0.f;
+        if (k & 1)
+            A2[k / 2].y = av, h[k / 2].y = hv;
+        else
+            A2[k / 2].x = av, h[k / 2].x = hv;
     }
     if (MODE == kLocalBwd) {
 #pragma unroll
-        for (int k = 0; k < NS / 2; ++k) po[k] = px[k] = f2(1.f), go[k] = gx[k] = f2(0.f);
+        for (int k = 0; k < NP; ++k) pr[k] = splat(1.f), g[k] = splat(0.f);
     }
     const float dtb = a.dtb != nullptr && cv ? __ldg(a.dtb + c) : 0.f;
     const float Dk = MODE == kOut && a.Dk != nullptr && cv ? __ldg(a.Dk + c) : 0.f;
-    const bool gate = a.z != nullptr && MODE != kLocal;
     float ssum = 0.f;
-    bool bad = false;
 
-    // requests of one tile: this thread's channel of kTok rows, its share of B and C
-    Walk wk(p0, a.H, a.W, a.dir);
-    uint16_t ru[kTok], rt[kTok], rz[kTok], ry[kTok], rb[kStage];
-    auto fetch = [&](int pb) {
+    // one token: t its step, x = t u, e (kLocalBwd); returns sum_n C h.  Each pair of states goes from
+    // its product to its update before the next begins: with the exponentials of a token or two
+    // ahead of the updates their pipe runs dry between bursts (97 us for 87 at 16384 tokens of 1024
+    // channels), and with a quarter of them taken by a polynomial the multiply-adds hold it up (88)
+    auto token = [&](int buf, int i, float t, float x, float e) -> float {
+        const float4 *B4 = reinterpret_cast<const float4 *>(bc[buf][0][i] + n0);
+        const float4 *C4 = reinterpret_cast<const float4 *>(bc[buf][1][i] + n0);
+        const float2 t2 = splat(t), x2 = splat(x), e2 = splat(e);
+        float2 y0 = splat(0.f), y1 = splat(0.f);
 #pragma unroll
-        for (int i = 0; i < kTok; ++i) {
-            const bool in = cv && pb + i < p1;
-            const long long row = row0 + wk.n;
-            ru[i] = ld16(a.u + row * a.ldu + c, in);
-            rt[i] = ld16(a.dt + row * a.lddt + c, in);
-            if (MODE != kLocal) rz[i] = ld16(a.z + row * a.ldz + c, in && gate);
-            if (MODE == kLocalBwd) ry[i] = ld16(a.dy + row * a.lddy + c, in);
-            wk.next();
-        }
+        for (int q = 0; q < NP / 2; ++q) {
+            const float4 Bq = B4[q];
+            const float4 Cq = MODE != kLocal ? C4[q] : Bq;
 #pragma unroll
-        for (int i = 0; i < kStage; ++i) {
-            const int e = tid + i * kThreads, n = e % SP, p = pb + e / SP % kTok;
-            const bool isc = e >= kTok * SP;
-            const bool in = p < p1 && n < a.S;
-            const long long row = row0 + token_of(in ? p : p0, a.H, a.W, a.dir);
-            rb[i] = isc ? ld16(a.cm + row * a.ldc + n, in && MODE != kLocal) : ld16(a.bm + row * a.ldb + n, in);
-        }
-    };
-    fetch(p0);
-    Walk wo(p0, a.H, a.W, a.dir);
-    int buf = 0;
-    for (int pb = p0; pb < p1; pb += kTok, buf ^= 1) {
-#pragma unroll
-        for (int i = 0; i < kStage; ++i) {
-            const int e = tid + i * kThreads;
-            bc[buf][e / (kTok * SP)][e / SP % kTok][e % SP] = Elem<T>::get(rb[i]);
-        }
-        float u[kTok], t[kTok], z[kTok], y[kTok];
-#pragma unroll
-        for (int i = 0; i < kTok; ++i) {
-            u[i] = Elem<T>::get(ru[i]);
-            const float raw = Elem<T>::get(rt[i]) + dtb;
-            t[i] = a.softplus ? softplus_f(raw) : raw;
-            if (MODE != kLocal) z[i] = Elem<T>::get(rz[i]);
-            if (MODE == kLocalBwd) y[i] = Elem<T>::get(ry[i]) * (gate ? z[i] * sigmoid_f(z[i]) : 1.f);
-        }
-        // one barrier a tile: a thread that writes buffer b again has passed the barrier of the
-        // tile between, which every thread reaches after its last read of b
-        __syncthreads();
-        fetch(pb + kTok);
-#pragma unroll
-        for (int i = 0; i < kTok; ++i) {
-            if (pb + i >= p1) break;   // the same for the whole block
-            const float x = t[i] * u[i];
-            const float tx = __shfl_xor_sync(0xffffffffu, t[i], 1), xx = __shfl_xor_sync(0xffffffffu, x, 1);
-            if (MODE != kOut) ssum += t[i];
-            float yx = 0.f;
-            if (MODE == kLocalBwd) yx = __shfl_xor_sync(0xffffffffu, y[i], 1);
-            float2 so = f2(0.f), sx = f2(0.f);
-            const float2 *B2 = reinterpret_cast<const float2 *>(&bc[buf][0][i][n0]);
-            const float2 *C2 = reinterpret_cast<const float2 *>(&bc[buf][1][i][n0]);
-#pragma unroll
-            for (int k = 0; k < NS / 2; ++k) {
-                const float2 Bk = B2[k];
-                float2 e = __fmul2_rn(f2(t[i]), Ao[k]);
-                float2 d = make_float2(ex2(e.x), ex2(e.y));
-                float2 e2 = __fmul2_rn(f2(tx), Ax[k]);
-                float2 d2 = make_float2(ex2(e2.x), ex2(e2.y));
-                ho[k] = __ffma2_rn(d, ho[k], __fmul2_rn(f2(x), Bk));
-                hx[k] = __ffma2_rn(d2, hx[k], __fmul2_rn(f2(xx), Bk));
-                if (MODE == kOut) {
-                    so = __ffma2_rn(C2[k], ho[k], so);
-                    sx = __ffma2_rn(C2[k], hx[k], sx);
-                }
+            for (int k = 2 * q; k < 2 * q + 2; ++k) {
+                const float2 Bk = k & 1 ? make_float2(Bq.z, Bq.w) : make_float2(Bq.x, Bq.y);
+                const float2 Ck = k & 1 ? make_float2(Cq.z, Cq.w) : make_float2(Cq.x, Cq.y);
+                const float2 m = __fmul2_rn(t2, A2[k]);
+                const float2 d = make_float2(ex2(m.x), ex2(m.y));
+                h[k] = __ffma2_rn(d, h[k], __fmul2_rn(x2, Bk));
+                if (MODE == kOut) (k & 1 ? y1 : y0) = __ffma2_rn(Ck, h[k], k & 1 ? y1 : y0);
                 if (MODE == kLocalBwd) {
-                    po[k] = __fmul2_rn(po[k], d);
-                    px[k] = __fmul2_rn(px[k], d2);
-                    go[k] = __ffma2_rn(po[k], __fmul2_rn(f2(y[i]), C2[k]), go[k]);
-                    gx[k] = __ffma2_rn(px[k], __fmul2_rn(f2(yx), C2[k]), gx[k]);
+                    pr[k] = __fmul2_rn(pr[k], d);
+                    g[k] = __ffma2_rn(pr[k], __fmul2_rn(e2, Ck), g[k]);
                 }
+            }
+        }
+        y0 = __fadd2_rn(y0, y1);
+        return y0.x + y0.y;
+    };
+
+    // this lane's first token of a group (butterfly below leaves the sums of its two tokens here)
+    const int own = 2 * sl;
+    auto tile = [&](auto full, int pb, int buf, int s) {
+        constexpr bool FULL = decltype(full)::value;
+#pragma unroll
+        for (int ig = 0; ig < TOK; ig += 2 * SL) {
+            if (!FULL && pb + ig >= p1) break;   // the same for the whole block
+            // the lanes of a channel each prepare two of 2 SL tokens
+            const int i = ig + own;
+            auto row2 = [&](int r) { return make_float2(Elem<T>::get(rows[s][r][i][cl]), Elem<T>::get(rows[s][r][i + 1][cl])); };
+            const float2 u = row2(0);
+            const float2 raw = __fadd2_rn(row2(1), splat(dtb));
+            float2 ex, t = softplus_2(raw, ex);   // selected, not branched over: one block of code
+            t = make_float2(sp_on ? t.x : raw.x, sp_on ? t.y : raw.y);
+            const float2 x = __fmul2_rn(t, u);
+            float2 sz = splat(1.f), e = splat(0.f);
+            if (MODE != kLocal) {
+                const float2 z = row2(MODE != kLocal ? 2 : 0);
+                sz = make_float2(z.x * sigmoid_f(z.x), z.y * sigmoid_f(z.y));
+                sz = make_float2(gate ? sz.x : 1.f, gate ? sz.y : 1.f);
+            }
+            if (MODE == kLocalBwd) e = __fmul2_rn(sz, row2(MODE == kLocalBwd ? 3 : 0));
+            float y[2 * SL];
+#pragma unroll
+            for (int o = 0; o < 2 * SL; ++o) {
+                y[o] = 0.f;
+                if (!FULL && o > 0 && pb + ig + o >= p1) break;
+                float to = o & 1 ? t.y : t.x, xo = o & 1 ? x.y : x.x;
+                if constexpr (SL > 1) {
+                    const int from = (tid & 31 & ~(SL - 1)) + o / 2;
+                    to = __shfl_sync(0xffffffffu, to, from);
+                    xo = __shfl_sync(0xffffffffu, xo, from);
+                }
+                if (MODE != kOut) ssum += to;
+                y[o] = token(buf, ig + o, to, xo, o & 1 ? e.y : e.x);
             }
             if (MODE == kOut) {
-                float s = so.x + so.y + __shfl_xor_sync(0xffffffffu, sx.x + sx.y, 1);
-                s = fmaf(Dk, u[i], s);
-                if (gate) s *= z[i] * sigmoid_f(z[i]);
-                if (cv) {
-                    a.out[(row0 + wo.n) * a.D + c] = Elem<T>::put(s);
-                    bad |= Elem<T>::bad(s);
-                }
-                wo.next();
+                if constexpr (SL > 1) butterfly<1, SL, 2 * SL>(y, tid & 31);
+                const float2 v = __fmul2_rn(__ffma2_rn(splat(Dk), u, make_float2(y[0], y[1])), sz);
+                outs[buf][MODE == kOut ? i : 0][MODE == kOut ? cl : 0] = Elem<T>::put(v.x);
+                outs[buf][MODE == kOut ? i + 1 : 0][MODE == kOut ? cl : 0] = Elem<T>::put(v.y);
             }
         }
+    };
+
+    int buf = 0, s = 0, before = 0;   // before: this thread's token of the tile before
+    for (int pb = p0; pb < p1; pb += TOK, buf ^= 1) {
+#pragma unroll
+        for (int i = 0; i < NBC; ++i) {
+            const int v = tc + RT * i;
+            bc[buf][v / SP][tt][v % SP] = Elem<T>::get(rb[i]);
+        }
+        if (WIDE) copy_wait<kStages - 2>();   // this tile's rows have landed
+        // one barrier a tile: what is written behind it (the next buffers of B, C and the outputs, the
+        // stage of the tile before) was last read ahead of it
+        __syncthreads();
+        load_bc(pb + TOK, tok[1]);
+        static_assert(kStages == 3, "tok holds the tokens of two tiles");
+        stage(pb + (kStages - 1) * TOK, s == 0 ? kStages - 1 : s - 1);
+        if (MODE == kOut) {
+            if (pb > p0) flush(pb - TOK, before, buf ^ 1);
+            before = tok[0];
+        }
+        tok[0] = tok[1];
+        tok[1] = wk.n;
+        wk.advance(TOK);
+        // whole tiles run without a branch, so that the scheduler can overlap their tokens
+        if (pb + TOK <= p1)
+            tile(std::true_type{}, pb, buf, s);
+        else
+            tile(std::false_type{}, pb, buf, s);
+        s = s == kStages - 1 ? 0 : s + 1;
     }
     if (MODE == kOut) {
+        __syncthreads();
+        flush(p0 + (p1 - 1 - p0) / TOK * TOK, before, buf ^ 1);
         if (bad) set_error(kOpsErrRange);
         if (j != a.P - 1 || a.hf == nullptr) return;
     }
-    float *dst = MODE == kOut ? a.hf + (long long)b * a.D * a.S : a.hs + ((long long)b * a.P + j) * a.D * SP;
-    const int ds = MODE == kOut ? a.S : SP;
+    if (!cv) return;
+    if (MODE == kOut) {
+        float *dst = a.hf + ((long long)b * a.D + c) * a.S + n0;
 #pragma unroll
-    for (int k = 0; k < NS; ++k) {
-        const int n = n0 + k;
-        if (MODE == kOut && n >= a.S) continue;
-        const float h1 = k & 1 ? ho[k / 2].y : ho[k / 2].x, h2 = k & 1 ? hx[k / 2].y : hx[k / 2].x;
-        if (cv) dst[(long long)c * ds + n] = h1;
-        if (cov) dst[(long long)co * ds + n] = h2;
-        if (MODE == kLocalBwd) {
-            float *gd = a.gs + ((long long)b * a.P + j) * a.D * SP;
-            if (cv) gd[(long long)c * SP + n] = k & 1 ? go[k / 2].y : go[k / 2].x;
-            if (cov) gd[(long long)co * SP + n] = k & 1 ? gx[k / 2].y : gx[k / 2].x;
-        }
+        for (int k = 0; k < 2 * NP; ++k)
+            if (n0 + k < a.S) dst[k] = k & 1 ? h[k / 2].y : h[k / 2].x;
+        return;
     }
-    if (MODE != kOut && cv) a.sdt[((long long)b * a.P + j) * a.D + c] = ssum;
+    const long long at = ((long long)b * a.P + j) * a.D + c;
+    float4 *dst = reinterpret_cast<float4 *>(a.hs + at * SP);
+#pragma unroll
+    for (int q = 0; q < SP / 4; ++q) dst[q] = make_float4(h[2 * q].x, h[2 * q].y, h[2 * q + 1].x, h[2 * q + 1].y);
+    if (MODE == kLocalBwd) {
+        float4 *gd = reinterpret_cast<float4 *>(a.gs + at * SP);
+#pragma unroll
+        for (int q = 0; q < SP / 4; ++q) gd[q] = make_float4(g[2 * q].x, g[2 * q].y, g[2 * q + 1].x, g[2 * q + 1].y);
+    }
+    a.sdt[at] = ssum;
 }
 
 // The chunks in order, one thread per (batch, channel, state).  Forward: hs[j] becomes the state
 // leaving chunk j.  Backward (from the last chunk): gs[j] becomes the gradient of the state
-// entering chunk j.  The loads of kFold chunks are issued before the chain uses the first.
-constexpr int kFold = 8;
-template <int SP, bool BWD>
-__global__ void __launch_bounds__(256) ssm_fold_kernel(const Args a) {
-    const long long per = (long long)a.D * SP;
-    const long long id = (long long)blockIdx.x * 256 + threadIdx.x;
-    const int b = (int)(id / per);
-    if (b >= a.B) return;
-    const long long e = id - b * per;
-    const int d = (int)(e / SP), n = (int)(e % SP);
-    const float A2 = n < a.S ? __ldg(a.A + (long long)d * a.S + n) * kLog2e : 0.f;
-    const float *sd = a.sdt + (long long)b * a.P * a.D + d;
-    const int m = a.P - 1;
-    {
-        float *hs = a.hs + (long long)b * a.P * per + e;
-        float h = a.h0 != nullptr && n < a.S ? a.h0[((long long)b * a.D + d) * a.S + n] : 0.f;
-        if (!BWD) hs[m * per] = h;   // the last slot is free: the entering state of chunk 0
-        for (int j0 = 0; j0 < m; j0 += kFold) {
-            float v[kFold], s[kFold];
+// entering chunk j.  The chain itself is short; what costs are the loads, so those of kFold chunks
+// are requested at once, ahead of the chain, and the blocks are small, so that a single sequence's
+// reach every SM.
+constexpr int kFold = 32, kFoldThreads = 64;
+template <bool REV>
+__device__ __forceinline__ void fold_chain(float *v0, const float *s0, long long vs, long long ss, int m, float A2, float x) {
+    // REV: j = m, m - 1, .., 1; else 0 .. m - 1
+    for (int j0 = 0; j0 < m; j0 += kFold) {
+        float v[kFold], s[kFold];
 #pragma unroll
-            for (int i = 0; i < kFold; ++i) {
-                const int j = min(j0 + i, m - 1);
-                v[i] = hs[j * per];
-                s[i] = sd[(long long)j * a.D];
-            }
-#pragma unroll
-            for (int i = 0; i < kFold; ++i)
-                if (j0 + i < m) {
-                    h = fmaf(ex2(A2 * s[i]), h, v[i]);
-                    hs[(j0 + i) * per] = h;
-                }
+        for (int i = 0; i < kFold; ++i) {
+            const int q = min(j0 + i, m - 1), j = REV ? m - q : q;
+            v[i] = v0[j * vs];
+            s[i] = s0[j * ss];
         }
+#pragma unroll
+        for (int i = 0; i < kFold; ++i)
+            if (j0 + i < m) {
+                x = fmaf(ex2(A2 * s[i]), x, v[i]);
+                v0[(REV ? m - (j0 + i) : j0 + i) * vs] = x;
+            }
     }
-    if (BWD) {
-        float *gs = a.gs + (long long)b * a.P * per + e;
-        float g = a.dfin != nullptr && n < a.S ? a.dfin[((long long)b * a.D + d) * a.S + n] : 0.f;
-        for (int j0 = m; j0 >= 1; j0 -= kFold) {
-            float v[kFold], s[kFold];
-#pragma unroll
-            for (int i = 0; i < kFold; ++i) {
-                const int j = max(j0 - i, 1);
-                v[i] = gs[j * per];
-                s[i] = sd[(long long)j * a.D];
-            }
-#pragma unroll
-            for (int i = 0; i < kFold; ++i)
-                if (j0 - i >= 1) {
-                    g = fmaf(ex2(A2 * s[i]), g, v[i]);
-                    gs[(j0 - i) * per] = g;
-                }
-        }
+}
+template <int SP, bool BWD>
+__global__ void __launch_bounds__(kFoldThreads) ssm_fold_kernel(const Args a) {
+    chain_wait();
+    const long long per = (long long)a.D * SP;
+    const long long id = (long long)blockIdx.x * kFoldThreads + threadIdx.x;
+    const int way = BWD ? (int)(id / (per * a.B)) : 0;   // backward: the states, then the gradients
+    const long long rest = id - way * per * a.B;
+    const int b = (int)(rest / per);
+    if (b >= a.B || way > 1) return;
+    const long long e = rest - b * per;
+    const int d = (int)(e / SP), n = (int)(e % SP);
+    const bool in = n < a.S;
+    const float A2 = in ? __ldg(a.A + (long long)d * a.S + n) * kLog2e : 0.f;
+    const float *sd = a.sdt + (long long)b * a.P * a.D + d;
+    const long long st = ((long long)b * a.D + d) * a.S + n;
+    const int m = a.P - 1;
+    if (way == 0) {
+        float *hs = a.hs + (long long)b * a.P * per + e;
+        const float h = a.h0 != nullptr && in ? a.h0[st] : 0.f;
+        if (!BWD) hs[m * per] = h;   // the last slot is free: the entering state of chunk 0
+        fold_chain<false>(hs, sd, per, a.D, m, A2, h);
+    } else {
+        fold_chain<true>(a.gs + (long long)b * a.P * per + e, sd, per, a.D, m, A2, a.dfin != nullptr && in ? a.dfin[st] : 0.f);
     }
 }
 
@@ -280,6 +399,7 @@ __global__ void __launch_bounds__(256) ssm_fold_kernel(const Args a) {
 template <typename T, int S>
 __global__ void __launch_bounds__(256) ssm_token_kernel(const Args a) {
     constexpr int SL = S / 4;
+    chain_wait();
     const long long id = (long long)blockIdx.x * 256 + threadIdx.x;
     const int q = (int)(id % SL);
     const long long ch = id / SL;

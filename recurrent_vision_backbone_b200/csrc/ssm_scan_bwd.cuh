@@ -26,36 +26,14 @@
 namespace gtr {
 namespace sc {
 
-constexpr int kSub = 4, kMaxChunkBwd = 64;
-
-// Sums over lanes whose index differs in the bits [LO, HI): v[0 .. NV - 1] of every lane.  While
-// a lane holds several values a round exchanges half of them; then whole values.  Lane l ends
-// with the sums of the values [idx, idx + left) in v[0 .. left - 1], where idx is returned.
-template <int LO, int HI, int NV>
-__device__ __forceinline__ int butterfly(float *v, int lane) {
-    if constexpr (LO >= HI) {
-        return 0;
-    } else if constexpr (NV > 1) {
-        const bool up = lane & LO;
-#pragma unroll
-        for (int i = 0; i < NV / 2; ++i) {
-            const float send = up ? v[i] : v[i + NV / 2], keep = up ? v[i + NV / 2] : v[i];
-            v[i] = keep + __shfl_xor_sync(0xffffffffu, send, LO);
-        }
-        return (up ? NV / 2 : 0) + butterfly<LO * 2, HI, NV / 2>(v, lane);
-    } else {
-        v[0] += __shfl_xor_sync(0xffffffffu, v[0], LO);
-        return butterfly<LO * 2, HI, 1>(v, lane);
-    }
-}
-__host__ __device__ constexpr int left_of(int nv, int lanes) { return nv > lanes ? nv / lanes : 1; }
+constexpr int kSub = 4, kMaxChunkBwd = 56;
 
 template <int SP>
 struct GradLayout {
     static constexpr int SL = SP / 4;            // lanes that share a channel pair
     static constexpr int CW = 64 / SL;           // channels of a warp
     static constexpr int CT = 4 * CW;            // channels of a block
-    static constexpr int NE = kSub * CW / 32;    // (token, channel) entries a lane prepares
+    static constexpr int NE = (kSub * CW / 2 + 31) / 32;   // (token, channel pair) entries a lane prepares
     // shared memory, floats: B, C of the chunk; checkpoints; per warp t, x, e and q, r, y; dB, dC
     static constexpr int stage = 6 * kSub * CW;
     static __host__ __device__ constexpr int floats(int L) {
@@ -63,11 +41,13 @@ struct GradLayout {
     }
 };
 
-template <typename T, int SP>
-__global__ void __launch_bounds__(kThreads) ssm_grad_kernel(const Args a) {
+template <typename T, int SP, bool PAIRS>   // PAIRS: rows of channels start on 4 bytes and are even
+__global__ void __launch_bounds__(kThreads, 3) ssm_grad_kernel(const Args a) {
     using Lay = GradLayout<SP>;
     constexpr int SL = Lay::SL, CW = Lay::CW, NE = Lay::NE;
     extern __shared__ __align__(16) float sm[];
+    chain_wait();
+    __shared__ int stok[kMaxChunkBwd];                           // tokens of the chunk
     const int L = a.L;
     float *sB = sm, *sC = sB + L * SP;
     float4 *ck = reinterpret_cast<float4 *>(sC + L * SP);        // [L / kSub][2][kThreads]
@@ -85,16 +65,19 @@ __global__ void __launch_bounds__(kThreads) ssm_grad_kernel(const Args a) {
     const int cb = ct * Lay::CT + warp * CW;     // the warp's first channel
     const int c = cb + 2 * pr;                   // this lane's channels: c, c + 1
     const bool cv[2] = {c < a.D, c + 1 < a.D};
-    const bool gate = a.z != nullptr;
+    const bool gate = a.z != nullptr, sp_on = a.softplus != 0;
 
+    if (tid < p1 - p0) stok[tid] = token_of(p0 + tid, a.H, a.W, a.dir);
+    __syncthreads();
     for (int i = tid; i < (p1 - p0) * SP; i += kThreads) {
         const int n = i % SP;
-        const long long row = row0 + token_of(p0 + i / SP, a.H, a.W, a.dir);
+        const long long row = row0 + stok[i / SP];
         sB[i] = Elem<T>::get(ld16(a.bm + row * a.ldb + n, n < a.S));
         sC[i] = Elem<T>::get(ld16(a.cm + row * a.ldc + n, n < a.S));
     }
 
-    float A2[2][4], h[2][4], g[2][4], dA[2][4];
+    // states in pairs: [channel][pair]
+    float2 A2[2][2], h[2][2], g[2][2], dA[2][2];
     {
         const float *hs = j > 0 ? a.hs + ((long long)b * a.P + j - 1) * a.D * SP
                                 : a.h0 != nullptr ? a.h0 + (long long)b * a.D * a.S : nullptr;
@@ -108,128 +91,178 @@ __global__ void __launch_bounds__(kThreads) ssm_grad_kernel(const Args a) {
             for (int i = 0; i < 4; ++i) {
                 const int n = sl * 4 + i;
                 const bool in = cv[k] && n < a.S;
-                A2[k][i] = in ? __ldg(a.A + (long long)(c + k) * a.S + n) * kLog2e : 0.f;
-                h[k][i] = in && hs != nullptr ? hs[(long long)(c + k) * hst + n] : 0.f;
-                g[k][i] = in && gs != nullptr ? gs[(long long)(c + k) * gst + n] : 0.f;
-                dA[k][i] = 0.f;
+                const float av = in ? __ldg(a.A + (long long)(c + k) * a.S + n) * kLog2e : 0.f;
+                const float hv = in && hs != nullptr ? hs[(long long)(c + k) * hst + n] : 0.f;
+                const float gv = in && gs != nullptr ? gs[(long long)(c + k) * gst + n] : 0.f;
+                if (i & 1)
+                    A2[k][i / 2].y = av, h[k][i / 2].y = hv, g[k][i / 2].y = gv;
+                else
+                    A2[k][i / 2].x = av, h[k][i / 2].x = hv, g[k][i / 2].x = gv;
+                dA[k][i / 2] = splat(0.f);
             }
     }
-    // the entries (token, channel) of a sub-chunk that this lane prepares: channel lane % CW of
-    // tokens lane / CW + (32 / CW) e
-    const int ec = cb + lane % CW;
-    const bool ecv = ec < a.D;
-    const float dtb = a.dtb != nullptr && ecv ? __ldg(a.dtb + ec) : 0.f;
-    const float Dk = a.Dk != nullptr && ecv ? __ldg(a.Dk + ec) : 0.f;
-    float accD = 0.f, accT = 0.f;
+    // the entries (token, channel pair) of a sub-chunk that this lane prepares: pair lane % (CW / 2)
+    // of tokens lane / (CW / 2) + (64 / CW) e; asked for one sub-chunk ahead
+    const int el = 2 * (lane % (CW / 2)), ec = cb + el;
+    const bool e0 = ec < a.D, e1 = ec + 1 < a.D;
+    auto param = [&](const float *p) {
+        return make_float2(p != nullptr && e0 ? __ldg(p + ec) : 0.f, p != nullptr && e1 ? __ldg(p + ec + 1) : 0.f);
+    };
+    const float2 dtb = param(a.dtb), Dk = param(a.Dk);
+    float2 accD = splat(0.f), accT = splat(0.f);
     bool bad = false;
+    uint32_t qu[NE], qt[NE], qy[NE], qz[NE];
+    auto pair_at = [&](const uint16_t *p, long long at, bool in) -> uint32_t {
+        if (PAIRS) return in && e0 ? __ldg(reinterpret_cast<const uint32_t *>(p + at)) : 0u;
+        return (uint32_t)ld16(p + at, in && e0) | (uint32_t)ld16(p + at + 1, in && e1) << 16;
+    };
+    auto put_pair = [&](uint16_t *p, long long at, float2 v) {
+        const uint32_t w = Elem<T>::put2(v.x, v.y);
+        bad |= e1 ? Elem<T>::bad_raw(w) : Elem<T>::bad_raw(w & 0xffffu);
+        if (PAIRS) {
+            *reinterpret_cast<uint32_t *>(p + at) = w;
+        } else {
+            p[at] = (uint16_t)w;
+            if (e1) p[at + 1] = (uint16_t)(w >> 16);
+        }
+    };
+    auto entry = [&](int e) { return (lane + 32 * e) / (CW / 2); };   // token of the sub-chunk
+    auto fetch = [&](int s, bool all) {
+#pragma unroll
+        for (int e = 0; e < NE; ++e) {
+            const int q = s * kSub + entry(e);
+            const bool in = s >= 0 && entry(e) < kSub && q < p1 - p0;
+            const long long row = row0 + (in ? stok[q] : 0);
+            qu[e] = pair_at(a.u, row * a.ldu + ec, in);
+            qt[e] = pair_at(a.dt, row * a.lddt + ec, in);
+            if (all) {
+                qy[e] = pair_at(a.dy, row * a.lddy + ec, in);
+                qz[e] = pair_at(a.z, row * a.ldz + ec, in && gate);
+            }
+        }
+    };
+    auto put2 = [](float *p, float2 v) { *reinterpret_cast<float2 *>(p) = v; };
+    // a token forward: the decays, and the states after it
+    auto forward = [&](int s, int tt, float2 (&d)[2][2]) {
+        const float2 t = *reinterpret_cast<const float2 *>(st + tt * CW + 2 * pr);
+        const float2 x = *reinterpret_cast<const float2 *>(sx + tt * CW + 2 * pr);
+        const float4 B = *reinterpret_cast<const float4 *>(sB + (s * kSub + tt) * SP + sl * 4);
+        const float2 Bv[2] = {make_float2(B.x, B.y), make_float2(B.z, B.w)};
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const float2 tk = splat(k ? t.y : t.x), xk = splat(k ? x.y : x.x);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const float2 m = __fmul2_rn(tk, A2[k][i]);
+                d[k][i] = make_float2(ex2(m.x), ex2(m.y));
+                h[k][i] = __ffma2_rn(d[k][i], h[k][i], __fmul2_rn(xk, Bv[i]));
+            }
+        }
+    };
     __syncthreads();
 
     // sweep: checkpoints of the states entering the sub-chunks
+    fetch(0, nsub == 1);
     for (int s = 0; s < nsub; ++s) {
-        ck[(s * 2 + 0) * kThreads + tid] = make_float4(h[0][0], h[0][1], h[0][2], h[0][3]);
-        ck[(s * 2 + 1) * kThreads + tid] = make_float4(h[1][0], h[1][1], h[1][2], h[1][3]);
+        ck[(s * 2 + 0) * kThreads + tid] = make_float4(h[0][0].x, h[0][0].y, h[0][1].x, h[0][1].y);
+        ck[(s * 2 + 1) * kThreads + tid] = make_float4(h[1][0].x, h[1][0].y, h[1][1].x, h[1][1].y);
         if (s == nsub - 1) break;
         __syncwarp();
 #pragma unroll
         for (int e = 0; e < NE; ++e) {   // every sub-chunk but the last is whole
-            const int tt = (lane + 32 * e) / CW;
-            const long long row = row0 + token_of(p0 + s * kSub + tt, a.H, a.W, a.dir);
-            const float raw = Elem<T>::get(ld16(a.dt + row * a.lddt + ec, ecv)) + dtb;
-            const float t = a.softplus ? softplus_f(raw) : raw;
-            st[tt * CW + lane % CW] = t;
-            sx[tt * CW + lane % CW] = t * Elem<T>::get(ld16(a.u + row * a.ldu + ec, ecv));
+            if (entry(e) >= kSub) break;
+            const int ix = entry(e) * CW + el;
+            const float2 raw = __fadd2_rn(Elem<T>::get2(qt[e]), dtb);
+            float2 x, t = softplus_2(raw, x);   // selected, not branched over
+            t = make_float2(sp_on ? t.x : raw.x, sp_on ? t.y : raw.y);
+            put2(st + ix, t);
+            put2(sx + ix, __fmul2_rn(t, Elem<T>::get2(qu[e])));
         }
         __syncwarp();
+        fetch(s + 1, s + 1 == nsub - 1);
+        float2 d[2][2];
 #pragma unroll
-        for (int tt = 0; tt < kSub; ++tt) {
-            const float2 t = *reinterpret_cast<const float2 *>(st + tt * CW + 2 * pr);
-            const float2 x = *reinterpret_cast<const float2 *>(sx + tt * CW + 2 * pr);
-            const float4 B = *reinterpret_cast<const float4 *>(sB + (s * kSub + tt) * SP + sl * 4);
-            const float Bv[4] = {B.x, B.y, B.z, B.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                h[0][i] = fmaf(ex2(t.x * A2[0][i]), h[0][i], x.x * Bv[i]);
-                h[1][i] = fmaf(ex2(t.y * A2[1][i]), h[1][i], x.y * Bv[i]);
-            }
-        }
+        for (int tt = 0; tt < kSub; ++tt) forward(s, tt, d);
     }
 
     // sub-chunks from the last to the first
-    for (int s = nsub - 1; s >= 0; --s) {
-        const int q0 = p0 + s * kSub, m = min(kSub, p1 - q0);
-        float eu[NE], et[NE], ee[NE], esg[NE], ez[NE], ey[NE];   // u, t, e, sigmoid(raw), z, d_out
-        long long er[NE];
+    // (whole ones without a branch inside, so that the scheduler can overlap their tokens)
+    auto sub = [&](auto full, int s) {
+        constexpr bool FULL = decltype(full)::value;
+        const int q0 = s * kSub, m = FULL ? kSub : p1 - p0 - q0;
+        float2 eu[NE], et[NE], ee[NE], esg[NE], ez[NE], esz[NE], ey[NE];   // u, t, e, dt / d raw, z, sigmoid(z), d_out
         __syncwarp();
 #pragma unroll
         for (int e = 0; e < NE; ++e) {
-            const int tt = (lane + 32 * e) / CW;
-            const bool in = ecv && tt < m;
-            er[e] = row0 + token_of(tt < m ? q0 + tt : q0, a.H, a.W, a.dir);
-            eu[e] = Elem<T>::get(ld16(a.u + er[e] * a.ldu + ec, in));
-            const float raw = Elem<T>::get(ld16(a.dt + er[e] * a.lddt + ec, in)) + dtb;
-            ey[e] = Elem<T>::get(ld16(a.dy + er[e] * a.lddy + ec, in));
-            ez[e] = Elem<T>::get(ld16(a.z + er[e] * a.ldz + ec, in && gate));
-            et[e] = a.softplus ? softplus_f(raw) : raw;
-            esg[e] = a.softplus ? sigmoid_f(raw) : 1.f;
-            ee[e] = gate ? ey[e] * (ez[e] * sigmoid_f(ez[e])) : ey[e];
-            st[tt * CW + lane % CW] = et[e];
-            sx[tt * CW + lane % CW] = et[e] * eu[e];
-            se[tt * CW + lane % CW] = ee[e];
+            if (entry(e) >= kSub) break;
+            const int ix = entry(e) * CW + el;
+            eu[e] = Elem<T>::get2(qu[e]);
+            ey[e] = Elem<T>::get2(qy[e]);
+            ez[e] = Elem<T>::get2(qz[e]);
+            const float2 raw = __fadd2_rn(Elem<T>::get2(qt[e]), dtb);
+            float2 x;
+            const float2 t = softplus_2(raw, x);
+            et[e] = make_float2(sp_on ? t.x : raw.x, sp_on ? t.y : raw.y);
+            esg[e] = make_float2(sp_on ? sigmoid_of(raw.x, x.x) : 1.f, sp_on ? sigmoid_of(raw.y, x.y) : 1.f);
+            esz[e] = make_float2(sigmoid_f(ez[e].x), sigmoid_f(ez[e].y));
+            const float2 eg = __fmul2_rn(ey[e], __fmul2_rn(ez[e], esz[e]));
+            ee[e] = make_float2(gate ? eg.x : ey[e].x, gate ? eg.y : ey[e].y);
+            put2(st + ix, et[e]);
+            put2(sx + ix, __fmul2_rn(et[e], eu[e]));
+            put2(se + ix, ee[e]);
         }
         __syncwarp();
-        float d[kSub][2][4], hp[kSub][2][4];   // decays; states entering the tokens
+        fetch(s - 1, true);
+        float2 d[kSub][2][2], hp[kSub][2][2];   // decays; states entering the tokens
         {
             const float4 c0 = ck[(s * 2 + 0) * kThreads + tid], c1 = ck[(s * 2 + 1) * kThreads + tid];
-            h[0][0] = c0.x, h[0][1] = c0.y, h[0][2] = c0.z, h[0][3] = c0.w;
-            h[1][0] = c1.x, h[1][1] = c1.y, h[1][2] = c1.z, h[1][3] = c1.w;
+            h[0][0] = make_float2(c0.x, c0.y), h[0][1] = make_float2(c0.z, c0.w);
+            h[1][0] = make_float2(c1.x, c1.y), h[1][1] = make_float2(c1.z, c1.w);
         }
 #pragma unroll
         for (int tt = 0; tt < kSub; ++tt) {
-            if (tt >= m) break;   // the same for the whole block
-            const float2 t = *reinterpret_cast<const float2 *>(st + tt * CW + 2 * pr);
-            const float2 x = *reinterpret_cast<const float2 *>(sx + tt * CW + 2 * pr);
-            const float4 B = *reinterpret_cast<const float4 *>(sB + (s * kSub + tt) * SP + sl * 4);
-            const float Bv[4] = {B.x, B.y, B.z, B.w};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                hp[tt][0][i] = h[0][i];
-                hp[tt][1][i] = h[1][i];
-                d[tt][0][i] = ex2(t.x * A2[0][i]);
-                d[tt][1][i] = ex2(t.y * A2[1][i]);
-                h[0][i] = fmaf(d[tt][0][i], h[0][i], x.x * Bv[i]);
-                h[1][i] = fmaf(d[tt][1][i], h[1][i], x.y * Bv[i]);
-            }
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) hp[tt][k][i] = h[k][i];   // behind the last token: the state after it
+            if (FULL || tt < m) forward(s, tt, d[tt]);   // the same for the whole block
         }
         float *ws = wsum + (s & 1) * 4 * kSub * 2 * SP + warp * kSub * 2 * SP;
 #pragma unroll
         for (int tt = kSub - 1; tt >= 0; --tt) {
-            if (tt >= m) continue;
+            if (!FULL && tt >= m) continue;
             const float2 t = *reinterpret_cast<const float2 *>(st + tt * CW + 2 * pr);
             const float2 x = *reinterpret_cast<const float2 *>(sx + tt * CW + 2 * pr);
             const float2 e = *reinterpret_cast<const float2 *>(se + tt * CW + 2 * pr);
-            const float4 B = *reinterpret_cast<const float4 *>(sB + (s * kSub + tt) * SP + sl * 4);
-            const float4 C = *reinterpret_cast<const float4 *>(sC + (s * kSub + tt) * SP + sl * 4);
-            const float Bv[4] = {B.x, B.y, B.z, B.w}, Cv[4] = {C.x, C.y, C.z, C.w};
-            float vbc[8];                                  // dB[4], dC[4] of this lane's channels
-            float vs[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};   // q, r, y of both, two unused
+            const float4 B = *reinterpret_cast<const float4 *>(sB + (q0 + tt) * SP + sl * 4);
+            const float4 C = *reinterpret_cast<const float4 *>(sC + (q0 + tt) * SP + sl * 4);
+            const float2 Bv[2] = {make_float2(B.x, B.y), make_float2(B.z, B.w)};
+            const float2 Cv[2] = {make_float2(C.x, C.y), make_float2(C.z, C.w)};
+            float2 vb[2], vc[2];                           // dB, dC of this lane's channels
+            float vs[8];                                   // q, r, y of both channels, two unused
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-                const float tk = k ? t.y : t.x, xk = k ? x.y : x.x, ek = k ? e.y : e.x;
+                const float2 tk = splat(k ? t.y : t.x), xk = splat(k ? x.y : x.x), ek = splat(k ? e.y : e.x);
+                float2 q = splat(0.f), r = splat(0.f), y = splat(0.f);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    // the state after the token: the next token's entering state, or the last
-                    const float hn = tt + 1 < kSub ? (tt + 1 < m ? hp[tt + 1 < kSub ? tt + 1 : tt][k][i] : h[k][i]) : h[k][i];
-                    const float G = fmaf(ek, Cv[i], g[k][i]);
-                    const float Ga = G * d[tt][k][i], w = Ga * hp[tt][k][i];
-                    vs[k] = fmaf(G, Bv[i], vs[k]);
-                    vs[2 + k] = fmaf(w, A2[k][i], vs[2 + k]);
-                    vs[4 + k] = fmaf(Cv[i], hn, vs[4 + k]);
-                    dA[k][i] = fmaf(w, tk, dA[k][i]);
-                    vbc[i] = k ? fmaf(G, xk, vbc[i]) : G * xk;
-                    vbc[4 + i] = k ? fmaf(ek, hn, vbc[4 + i]) : ek * hn;
+                for (int i = 0; i < 2; ++i) {
+                    const float2 hn = tt + 1 < kSub ? hp[tt + 1 < kSub ? tt + 1 : tt][k][i] : h[k][i];   // after the token
+                    const float2 G = __ffma2_rn(ek, Cv[i], g[k][i]);
+                    const float2 Ga = __fmul2_rn(G, d[tt][k][i]), w = __fmul2_rn(Ga, hp[tt][k][i]);
+                    q = __ffma2_rn(G, Bv[i], q);
+                    r = __ffma2_rn(w, A2[k][i], r);
+                    y = __ffma2_rn(Cv[i], hn, y);
+                    dA[k][i] = __ffma2_rn(w, tk, dA[k][i]);
+                    vb[i] = k ? __ffma2_rn(G, xk, vb[i]) : __fmul2_rn(G, xk);
+                    vc[i] = k ? __ffma2_rn(ek, hn, vc[i]) : __fmul2_rn(ek, hn);
                     g[k][i] = Ga;
                 }
+                vs[k] = q.x + q.y;
+                vs[2 + k] = r.x + r.y;
+                vs[4 + k] = y.x + y.y;
+                vs[6 + k] = 0.f;
             }
+            float vbc[8] = {vb[0].x, vb[0].y, vb[1].x, vb[1].y, vc[0].x, vc[0].y, vc[1].x, vc[1].y};
             const int ib = butterfly<SL, 32, 8>(vbc, lane);   // over the channels of the warp
             constexpr int lb = left_of(8, 32 / SL);
 #pragma unroll
@@ -248,31 +281,34 @@ __global__ void __launch_bounds__(kThreads) ssm_grad_kernel(const Args a) {
         __syncthreads();   // the warps' sums of dB, dC (two buffers: the next sub-chunk writes the other)
         for (int i = tid; i < m * 2 * SP; i += kThreads) {
             const float *w0 = wsum + (s & 1) * 4 * kSub * 2 * SP + i;
-            const float v = w0[0] + w0[kSub * 2 * SP] + w0[2 * kSub * 2 * SP] + w0[3 * kSub * 2 * SP];
-            const long long row = row0 + token_of(q0 + i / (2 * SP), a.H, a.W, a.dir);
+            const float v = (w0[0] + w0[kSub * 2 * SP]) + (w0[2 * kSub * 2 * SP] + w0[3 * kSub * 2 * SP]);
+            const long long row = row0 + stok[q0 + i / (2 * SP)];
             a.pbc[((long long)ct * a.B * a.N + row) * 2 * SP + i % (2 * SP)] = v;
         }
 #pragma unroll
         for (int e = 0; e < NE; ++e) {
-            const int tt = (lane + 32 * e) / CW, ix = tt * CW + lane % CW;
-            if (!ecv || tt >= m) continue;
-            const float q = rq[ix], r = rr[ix] * kLn2;   // A2 = A log2(e)
-            const float du = fmaf(q, et[e], Dk * ee[e]);
-            const float dr = fmaf(q, eu[e], r) * esg[e];
-            accD = fmaf(ee[e], eu[e], accD);
-            accT += dr;
-            const long long o = er[e] * a.D + ec;
-            a.du[o] = Elem<T>::put(du);
-            a.ddt[o] = Elem<T>::put(dr);
-            bad |= Elem<T>::bad(du) | Elem<T>::bad(dr);
+            if (!e0 || entry(e) >= m) continue;
+            const int ix = entry(e) * CW + el;
+            const float2 q = *reinterpret_cast<const float2 *>(rq + ix);
+            const float2 r = __fmul2_rn(*reinterpret_cast<const float2 *>(rr + ix), splat(kLn2));   // A2 = A log2(e)
+            const float2 dr = __fmul2_rn(__ffma2_rn(q, eu[e], r), esg[e]);
+            accD = __ffma2_rn(ee[e], eu[e], accD);
+            accT = __fadd2_rn(accT, dr);
+            const long long o = (row0 + stok[q0 + entry(e)]) * a.D + ec;
+            put_pair(a.du, o, __ffma2_rn(q, et[e], __fmul2_rn(Dk, ee[e])));
+            put_pair(a.ddt, o, dr);
             if (gate) {
-                const float y = fmaf(Dk, eu[e], ry[ix]), sg = sigmoid_f(ez[e]);
-                const float dz = ey[e] * y * (sg * fmaf(ez[e], 1.f - sg, 1.f));
-                a.dz[o] = Elem<T>::put(dz);
-                bad |= Elem<T>::bad(dz);
+                const float2 y = __ffma2_rn(Dk, eu[e], *reinterpret_cast<const float2 *>(ry + ix)), sg = esz[e];
+                const float2 one = __ffma2_rn(ez[e], __fadd2_rn(splat(1.f), make_float2(-sg.x, -sg.y)), splat(1.f));
+                put_pair(a.dz, o, __fmul2_rn(__fmul2_rn(ey[e], y), __fmul2_rn(sg, one)));
             }
         }
-    }
+    };
+    if ((p1 - p0) % kSub != 0)
+        sub(std::false_type{}, nsub - 1);
+    else
+        sub(std::true_type{}, nsub - 1);
+    for (int s = nsub - 2; s >= 0; --s) sub(std::true_type{}, s);
     if (bad) set_error(kOpsErrRange);
 
     // the chunk's share of dA over the state slot that only this chunk reads (chunk 0: the last
@@ -282,21 +318,25 @@ __global__ void __launch_bounds__(kThreads) ssm_grad_kernel(const Args a) {
     for (int k = 0; k < 2; ++k) {
         if (!cv[k]) continue;
         *reinterpret_cast<float4 *>(pa + (long long)(c + k) * SP + sl * 4) =
-            make_float4(dA[k][0], dA[k][1], dA[k][2], dA[k][3]);
+            make_float4(dA[k][0].x, dA[k][0].y, dA[k][1].x, dA[k][1].y);
         if (j == 0 && a.dh0 != nullptr) {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                if (sl * 4 + i < a.S) a.dh0[((long long)b * a.D + c + k) * a.S + sl * 4 + i] = g[k][i];
+                if (sl * 4 + i < a.S)
+                    a.dh0[((long long)b * a.D + c + k) * a.S + sl * 4 + i] = i & 1 ? g[k][i / 2].y : g[k][i / 2].x;
         }
     }
 #pragma unroll
-    for (int o = CW; o < 32; o *= 2) {
-        accD += __shfl_xor_sync(0xffffffffu, accD, o);
-        accT += __shfl_xor_sync(0xffffffffu, accT, o);
+    for (int o = CW / 2; o < 32; o *= 2) {
+        accD.x += __shfl_xor_sync(0xffffffffu, accD.x, o);
+        accD.y += __shfl_xor_sync(0xffffffffu, accD.y, o);
+        accT.x += __shfl_xor_sync(0xffffffffu, accT.x, o);
+        accT.y += __shfl_xor_sync(0xffffffffu, accT.y, o);
     }
-    if (lane < CW && ecv) {
-        a.pd[((long long)b * a.P + j) * a.D + ec] = accD;
-        a.pt[((long long)b * a.P + j) * a.D + ec] = accT;
+    if (lane < CW / 2) {
+        const long long at = ((long long)b * a.P + j) * a.D + ec;
+        if (e0) a.pd[at] = accD.x, a.pt[at] = accT.x;
+        if (e1) a.pd[at + 1] = accD.y, a.pt[at + 1] = accT.y;
     }
 }
 
@@ -306,6 +346,7 @@ __global__ void __launch_bounds__(kThreads) ssm_grad_kernel(const Args a) {
 template <typename T, int SP>
 __global__ void __launch_bounds__(256) ssm_grad_sum_kernel(const Args a, int bc_blocks) {
     __shared__ float red[8][33];
+    chain_wait();
     if ((int)blockIdx.x < bc_blocks) {
         const long long id = (long long)blockIdx.x * 256 + threadIdx.x, rows = (long long)a.B * a.N;
         const long long row = id / (2 * SP);

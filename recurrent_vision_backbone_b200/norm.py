@@ -2,12 +2,10 @@
 (argument marshalling only; every step runs in the CUDA library)."""
 from __future__ import annotations
 
-import ctypes
-
 import torch
 
-from .gla import _ptr, _stream_handle, load
-from .ssm import ACT_NONE, ACT_SILU, DTYPES, _check, _dense, _device, _new, _workspace  # noqa: F401
+from .gla import load
+from .ssm import ACT_NONE, ACT_SILU, DTYPES, _check, _dense, _device, _new, _stream, _workspace  # noqa: F401
 
 
 def _shape(x, groups, gamma, beta):
@@ -15,16 +13,14 @@ def _shape(x, groups, gamma, beta):
         raise ValueError("x must be [B, ..., C]")
     if x.dtype not in DTYPES or not x.is_contiguous():
         raise ValueError("x must be a contiguous float16 or bfloat16 tensor")
-    _device(x, "x")
+    dev = _device(x, "x")
     B, C = x.shape[0], x.shape[-1]
     N = 1
     for n in x.shape[1:-1]:
         N *= n
     if groups <= 0 or C == 0 or C % groups:
         raise ValueError(f"{groups} groups do not divide {C} channels")
-    _dense(gamma, "gamma", (C,), torch.float32, required=False)
-    _dense(beta, "beta", (C,), torch.float32, required=False)
-    return B, N, C
+    return B, N, C, dev, _dense(gamma, "gamma", (C,), torch.float32, dev, False), _dense(beta, "beta", (C,), torch.float32, dev, False)
 
 
 def group_norm_fwd_workspace_bytes(B: int, N: int, C: int, groups: int) -> int:
@@ -46,18 +42,16 @@ def gtr_group_norm_fwd(x, groups: int, gamma=None, beta=None, eps: float = 1e-5,
     reciprocal deviations (the backward pass takes it) or None to allocate one; workspace: a CUDA
     tensor of group_norm_fwd_workspace_bytes(...) bytes, or None to allocate one.  Returns
     (out, stats)."""
-    lib = load()
-    B, N, C = _shape(x, groups, gamma, beta)
+    B, N, C, dev, gp, bp = _shape(x, groups, gamma, beta)
     if out is None:
-        out = _new(x.shape, x.dtype, x.device, stream)
-    _dense(out, "out", x.shape, x.dtype)
+        out = _new(x, x.shape, x.dtype, stream)
     if stats is None:
-        stats = _new((B, groups, 2), torch.float32, x.device, stream)
-    _dense(stats, "stats", (B, groups, 2), torch.float32)
-    ws, nbytes = _workspace(workspace, group_norm_fwd_workspace_bytes(B, N, C, groups), x.device, stream)
-    _check(lib.gtr_group_norm_fwd(_ptr(x), _ptr(gamma), _ptr(beta), B, N, C, groups, ctypes.c_float(eps),
-                                  DTYPES[x.dtype], int(activation), _ptr(out), _ptr(stats), _ptr(ws), nbytes,
-                                  _stream_handle(stream)), "gtr_group_norm_fwd")
+        stats = _new(x, (B, groups, 2), torch.float32, stream)
+    ws, wp, nbytes = _workspace(workspace, group_norm_fwd_workspace_bytes(B, N, C, groups), x, stream)
+    _check(load().gtr_group_norm_fwd(x.data_ptr(), gp, bp, B, N, C, groups, eps, DTYPES[x.dtype], int(activation),
+                                     _dense(out, "out", x.shape, x.dtype, dev),
+                                     _dense(stats, "stats", (B, groups, 2), torch.float32, dev), wp, nbytes,
+                                     _stream(stream)), "gtr_group_norm_fwd")
     return out, stats
 
 
@@ -67,20 +61,16 @@ def gtr_group_norm_bwd(x, d_out, stats, groups: int, gamma=None, beta=None, acti
     CUDA tensor of group_norm_bwd_workspace_bytes(...) bytes, or None to allocate one.  grads:
     (grad_x, grad_gamma, grad_beta) to fill, or None to allocate them (those of absent parameters
     stay None).  Returns that tuple: grad_x of x's type, the others float32."""
-    lib = load()
-    B, N, C = _shape(x, groups, gamma, beta)
-    _dense(d_out, "d_out", x.shape, x.dtype)
-    _dense(stats, "stats", (B, groups, 2), torch.float32)
+    B, N, C, dev, gp, bp = _shape(x, groups, gamma, beta)
     if grads is None:
-        new = lambda shape, t: _new(shape, t, x.device, stream)  # noqa: E731
-        grads = (new(x.shape, x.dtype), None if gamma is None else new((C,), torch.float32),
-                 None if beta is None else new((C,), torch.float32))
+        grads = (_new(x, x.shape, x.dtype, stream), None if gamma is None else _new(x, (C,), torch.float32, stream),
+                 None if beta is None else _new(x, (C,), torch.float32, stream))
     gx, gg, gb = grads
-    _dense(gx, "grad_x", x.shape, x.dtype)
-    _dense(gg, "grad_gamma", (C,), torch.float32, required=False)
-    _dense(gb, "grad_beta", (C,), torch.float32, required=False)
-    ws, nbytes = _workspace(workspace, group_norm_bwd_workspace_bytes(B, N, C, groups), x.device, stream)
-    _check(lib.gtr_group_norm_bwd(_ptr(x), _ptr(d_out), _ptr(stats), _ptr(gamma), _ptr(beta), B, N, C, groups,
-                                  DTYPES[x.dtype], int(activation), _ptr(gx), _ptr(gg), _ptr(gb), _ptr(ws), nbytes,
-                                  _stream_handle(stream)), "gtr_group_norm_bwd")
+    ws, wp, nbytes = _workspace(workspace, group_norm_bwd_workspace_bytes(B, N, C, groups), x, stream)
+    _check(load().gtr_group_norm_bwd(x.data_ptr(), _dense(d_out, "d_out", x.shape, x.dtype, dev),
+                                     _dense(stats, "stats", (B, groups, 2), torch.float32, dev), gp, bp, B, N, C, groups,
+                                     DTYPES[x.dtype], int(activation), _dense(gx, "grad_x", x.shape, x.dtype, dev),
+                                     _dense(gg, "grad_gamma", (C,), torch.float32, dev, False),
+                                     _dense(gb, "grad_beta", (C,), torch.float32, dev, False), wp, nbytes,
+                                     _stream(stream)), "gtr_group_norm_bwd")
     return grads

@@ -14,8 +14,7 @@ import ctypes
 
 import torch
 
-from . import gla
-from .gla import B2T, GTR_OK, L2R, R2L, T2B, GTRError, _ptr, _stream_handle, load  # noqa: F401
+from .gla import B2T, GTR_OK, L2R, R2L, T2B, GTRError, load  # noqa: F401
 
 ACT_NONE, ACT_SILU = 0, 1
 DTYPES = {torch.float16: 0, torch.bfloat16: 1}
@@ -41,32 +40,33 @@ class _SsmGrads(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("u", "dt", "Bm", "Cm", "z", "A", "Dskip", "dt_bias", "init_state")]
 
 
+# Checks are spelled for speed: a call of one token takes a few microseconds on the GPU, so the
+# host side of a call is kept to the reads of tensor metadata that the checks need.
 def _addr(t):
     return None if t is None else t.data_ptr()
-
-
-def _on(stream):
-    """Allocations inside belong to the stream the call runs on."""
-    return torch.cuda.stream(stream)     # a no-op for None
 
 
 def _device(t, name):
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     cur = torch.cuda.current_device()
-    if t.device.index != cur:
+    if t.get_device() != cur:
         raise ValueError(f"{name} is on {t.device}, but the current CUDA device is cuda:{cur}")
+    return cur
 
 
-def _rows(t, name, shape, dtype):
-    """Checks a [B, N, cols] activation; returns the elements between its token rows."""
-    if tuple(t.shape) != tuple(shape):
+def _rows(t, name, shape, dtype, dev):
+    """Checks a [B, N, cols] activation on device `dev`; returns the elements between its token rows."""
+    if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, not {list(t.shape)}")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, like the other activations")
-    _device(t, name)
+    if t.get_device() != dev:
+        _device(t, name)
+    if t.is_contiguous():
+        return shape[2]
     B, N, cols = shape
-    if t.numel() == 0:
+    if B == 0 or N == 0:
         return 0
     sb, sn, sc = t.stride()
     if cols > 1 and sc != 1:
@@ -77,14 +77,16 @@ def _rows(t, name, shape, dtype):
     return ld
 
 
-def _dense(t, name, shape, dtype, required=True):
+def _dense(t, name, shape, dtype, dev, required=True):
     if t is None:
         if required:
             raise ValueError(f"{name} is required")
-        return
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or not t.is_contiguous():
+        return None
+    if t.shape != shape or t.dtype is not dtype or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor {list(shape)}")
-    _device(t, name)
+    if t.get_device() != dev:
+        _device(t, name)
+    return t.data_ptr()
 
 
 def _grid(x, name, Hgrid, Wgrid):
@@ -94,25 +96,32 @@ def _grid(x, name, Hgrid, Wgrid):
         raise ValueError(f"{name} must be float16 or bfloat16")
     if x.shape[1] != Hgrid * Wgrid:
         raise ValueError(f"N={x.shape[1]} does not match the grid {Hgrid}x{Wgrid}")
-    _device(x, name)
-    return x.shape
+    return x.shape, _device(x, name)
 
 
-def _workspace(t, nbytes, device, stream):
+def _new(like, shape, dtype, stream):
+    """A tensor on `like`'s device that belongs to the stream the call runs on."""
+    if stream is None:
+        return like.new_empty(shape, dtype=dtype)
+    with torch.cuda.stream(stream):
+        return like.new_empty(shape, dtype=dtype)
+
+
+def _workspace(t, nbytes, like, stream):
+    """(tensor, address, bytes) of the caller's workspace or a new one."""
     if nbytes == 0:
-        return None, 0
+        return None, None, 0
     if t is None:
-        with _on(stream):
-            t = torch.empty(nbytes, dtype=torch.uint8, device=device)
-    _device(t, "workspace")
-    if not t.is_contiguous():
-        raise ValueError("workspace must be contiguous")
-    return t, t.numel() * t.element_size()
+        t = _new(like, (nbytes,), torch.uint8, stream)
+    else:
+        _device(t, "workspace")
+        if not t.is_contiguous():
+            raise ValueError("workspace must be contiguous")
+    return t, t.data_ptr(), t.numel() * t.element_size()
 
 
-def _new(shape, dtype, device, stream):
-    with _on(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+def _stream(stream):
+    return torch.cuda.current_stream().cuda_stream if stream is None else stream.cuda_stream
 
 
 def _check(status, where):
@@ -122,17 +131,15 @@ def _check(status, where):
 
 # ------------------------------------------------------------------ short causal convolution
 def _conv(x, w, Hgrid, Wgrid, direction, bias, activation, init_state):
-    B, N, D = _grid(x, "x", Hgrid, Wgrid)
-    ld = _rows(x, "x", (B, N, D), x.dtype)
+    (B, N, D), dev = _grid(x, "x", Hgrid, Wgrid)
+    ld = _rows(x, "x", (B, N, D), x.dtype, dev)
     if w.dim() != 2:
         raise ValueError("w must be [D, K]")
     K = w.shape[1]
-    _dense(w, "w", (D, K), torch.float32)
-    _dense(bias, "bias", (D,), torch.float32, required=False)
-    _dense(init_state, "init_state", (B, K - 1, D), x.dtype, required=False)
-    c = _Conv(B, int(Hgrid), int(Wgrid), D, K, int(direction), DTYPES[x.dtype], int(activation), _addr(x), ld,
-              _addr(w), _addr(bias), _addr(init_state))
-    return c, (B, N, D, K)
+    c = _Conv(B, int(Hgrid), int(Wgrid), D, K, int(direction), DTYPES[x.dtype], int(activation), x.data_ptr(), ld,
+              _dense(w, "w", (D, K), torch.float32, dev), _dense(bias, "bias", (D,), torch.float32, dev, False),
+              _dense(init_state, "init_state", (B, K - 1, D), x.dtype, dev, False))
+    return c, (B, N, D, K), dev
 
 
 def gtr_causal_conv_fwd(x, w, Hgrid: int, Wgrid: int, direction: int, bias=None, activation: int = ACT_SILU,
@@ -144,16 +151,14 @@ def gtr_causal_conv_fwd(x, w, Hgrid: int, Wgrid: int, direction: int, bias=None,
     float32 [D] or None; init_state: the K - 1 earlier inputs, oldest first, [B, K-1, D] of x's
     type, or None for zeros; final_state: a tensor to fill (init_state itself for an in-place
     carry), True to allocate one, or None.  Returns (out, final_state)."""
-    lib = load()
-    c, (B, N, D, K) = _conv(x, w, Hgrid, Wgrid, direction, bias, activation, init_state)
+    c, (B, N, D, K), dev = _conv(x, w, Hgrid, Wgrid, direction, bias, activation, init_state)
     if out is None:
-        out = _new((B, N, D), x.dtype, x.device, stream)
-    _dense(out, "out", (B, N, D), x.dtype)
+        out = _new(x, (B, N, D), x.dtype, stream)
     if final_state is True:
-        final_state = _new((B, max(K - 1, 0), D), x.dtype, x.device, stream)
-    _dense(final_state, "final_state", (B, K - 1, D), x.dtype, required=False)
-    _check(lib.gtr_causal_conv_fwd(ctypes.byref(c), _ptr(out), _ptr(final_state), _stream_handle(stream)),
-           "gtr_causal_conv_fwd")
+        final_state = _new(x, (B, max(K - 1, 0), D), x.dtype, stream)
+    _check(load().gtr_causal_conv_fwd(ctypes.byref(c), _dense(out, "out", (B, N, D), x.dtype, dev),
+                                      _dense(final_state, "final_state", (B, K - 1, D), x.dtype, dev, False),
+                                      _stream(stream)), "gtr_causal_conv_fwd")
     return out, final_state
 
 
@@ -170,44 +175,38 @@ def gtr_causal_conv_bwd(x, w, d_out, Hgrid: int, Wgrid: int, direction: int, bia
     allocate one.  grads: (grad_x, grad_w, grad_bias, grad_init_state) to fill, or None to allocate
     them (grad_bias with a bias, grad_init_state with want_init_grad).  Returns that tuple:
     grad_x and grad_init_state of x's type, the parameters' float32."""
-    lib = load()
-    c, (B, N, D, K) = _conv(x, w, Hgrid, Wgrid, direction, bias, activation, init_state)
-    ld = _rows(d_out, "d_out", (B, N, D), x.dtype)
-    _dense(d_final_state, "d_final_state", (B, K - 1, D), x.dtype, required=False)
+    c, (B, N, D, K), dev = _conv(x, w, Hgrid, Wgrid, direction, bias, activation, init_state)
+    ld = _rows(d_out, "d_out", (B, N, D), x.dtype, dev)
+    df = _dense(d_final_state, "d_final_state", (B, K - 1, D), x.dtype, dev, False)
     if grads is None:
-        new = lambda shape, t: _new(shape, t, x.device, stream)  # noqa: E731
-        grads = (new((B, N, D), x.dtype), new((D, K), torch.float32),
-                 None if bias is None else new((D,), torch.float32),
-                 new((B, max(K - 1, 0), D), x.dtype) if want_init_grad else None)
+        grads = (_new(x, (B, N, D), x.dtype, stream), _new(x, (D, K), torch.float32, stream),
+                 None if bias is None else _new(x, (D,), torch.float32, stream),
+                 _new(x, (B, max(K - 1, 0), D), x.dtype, stream) if want_init_grad else None)
     gx, gw, gb, gi = grads
-    _dense(gx, "grad_x", (B, N, D), x.dtype)
-    _dense(gw, "grad_w", (D, K), torch.float32)
-    _dense(gb, "grad_bias", (D,), torch.float32, required=False)
-    _dense(gi, "grad_init_state", (B, K - 1, D), x.dtype, required=False)
-    ws, nbytes = _workspace(workspace, causal_conv_bwd_workspace_bytes(B, Hgrid, Wgrid, D, K), x.device, stream)
-    _check(lib.gtr_causal_conv_bwd(ctypes.byref(c), _ptr(d_out), ld, _ptr(d_final_state), _ptr(gx), _ptr(gw), _ptr(gb),
-                                   _ptr(gi), _ptr(ws), nbytes, _stream_handle(stream)), "gtr_causal_conv_bwd")
+    ws, wp, nbytes = _workspace(workspace, causal_conv_bwd_workspace_bytes(B, Hgrid, Wgrid, D, K), x, stream)
+    _check(load().gtr_causal_conv_bwd(ctypes.byref(c), d_out.data_ptr(), ld, df,
+                                      _dense(gx, "grad_x", (B, N, D), x.dtype, dev),
+                                      _dense(gw, "grad_w", (D, K), torch.float32, dev),
+                                      _dense(gb, "grad_bias", (D,), torch.float32, dev, False),
+                                      _dense(gi, "grad_init_state", (B, K - 1, D), x.dtype, dev, False), wp, nbytes,
+                                      _stream(stream)), "gtr_causal_conv_bwd")
     return gx, gw, gb, gi
 
 
 # ------------------------------------------------------------------ selective scan
 def _ssm(u, dt, A, Bm, Cm, Hgrid, Wgrid, direction, D, z, dt_bias, dt_softplus, init_state):
-    B, N, C = _grid(u, "u", Hgrid, Wgrid)
+    (B, N, C), dev = _grid(u, "u", Hgrid, Wgrid)
     if A.dim() != 2:
         raise ValueError("A must be [D, S]")
     S = A.shape[1]
-    t = u.dtype
-    ldu, lddt = _rows(u, "u", (B, N, C), t), _rows(dt, "dt", (B, N, C), t)
-    ldb, ldc = _rows(Bm, "Bm", (B, N, S), t), _rows(Cm, "Cm", (B, N, S), t)
-    ldz = 0 if z is None else _rows(z, "z", (B, N, C), t)
-    _dense(A, "A", (C, S), torch.float32)
-    _dense(D, "D", (C,), torch.float32, required=False)
-    _dense(dt_bias, "dt_bias", (C,), torch.float32, required=False)
-    _dense(init_state, "init_state", (B, C, S), torch.float32, required=False)
-    m = _Ssm(B, int(Hgrid), int(Wgrid), C, S, int(direction), DTYPES[t], int(bool(dt_softplus)), _addr(u), _addr(dt),
-             _addr(Bm), _addr(Cm), _addr(z), ldu, lddt, ldb, ldc, ldz, _addr(A), _addr(D), _addr(dt_bias),
-             _addr(init_state))
-    return m, (B, N, C, S)
+    t, f, tok, st = u.dtype, torch.float32, (B, N, C), (B, N, S)
+    m = _Ssm(B, int(Hgrid), int(Wgrid), C, S, int(direction), DTYPES[t], int(bool(dt_softplus)), u.data_ptr(),
+             dt.data_ptr(), Bm.data_ptr(), Cm.data_ptr(), _addr(z), _rows(u, "u", tok, t, dev),
+             _rows(dt, "dt", tok, t, dev), _rows(Bm, "Bm", st, t, dev), _rows(Cm, "Cm", st, t, dev),
+             0 if z is None else _rows(z, "z", tok, t, dev), _dense(A, "A", (C, S), f, dev),
+             _dense(D, "D", (C,), f, dev, False), _dense(dt_bias, "dt_bias", (C,), f, dev, False),
+             _dense(init_state, "init_state", (B, C, S), f, dev, False))
+    return m, (B, N, C, S), dev
 
 
 def ssm_scan_fwd_workspace_bytes(B: int, Hgrid: int, Wgrid: int, D: int, S: int) -> int:
@@ -226,17 +225,15 @@ def gtr_ssm_scan_fwd(u, dt, A, Bm, Cm, Hgrid: int, Wgrid: int, direction: int, D
     fill (init_state itself for an in-place carry), True to allocate one, or None; workspace: a
     CUDA tensor of ssm_scan_fwd_workspace_bytes(...) bytes, or None to allocate one.  Returns
     (out, final_state)."""
-    lib = load()
-    m, (B, N, C, S) = _ssm(u, dt, A, Bm, Cm, Hgrid, Wgrid, direction, D, z, dt_bias, dt_softplus, init_state)
+    m, (B, N, C, S), dev = _ssm(u, dt, A, Bm, Cm, Hgrid, Wgrid, direction, D, z, dt_bias, dt_softplus, init_state)
     if out is None:
-        out = _new((B, N, C), u.dtype, u.device, stream)
-    _dense(out, "out", (B, N, C), u.dtype)
+        out = _new(u, (B, N, C), u.dtype, stream)
     if final_state is True:
-        final_state = _new((B, C, S), torch.float32, u.device, stream)
-    _dense(final_state, "final_state", (B, C, S), torch.float32, required=False)
-    ws, nbytes = _workspace(workspace, ssm_scan_fwd_workspace_bytes(B, Hgrid, Wgrid, C, S), u.device, stream)
-    _check(lib.gtr_ssm_scan_fwd(ctypes.byref(m), _ptr(out), _ptr(final_state), _ptr(ws), nbytes,
-                                _stream_handle(stream)), "gtr_ssm_scan_fwd")
+        final_state = _new(u, (B, C, S), torch.float32, stream)
+    ws, wp, nbytes = _workspace(workspace, ssm_scan_fwd_workspace_bytes(B, Hgrid, Wgrid, C, S), u, stream)
+    _check(load().gtr_ssm_scan_fwd(ctypes.byref(m), _dense(out, "out", (B, N, C), u.dtype, dev),
+                                   _dense(final_state, "final_state", (B, C, S), torch.float32, dev, False), wp, nbytes,
+                                   _stream(stream)), "gtr_ssm_scan_fwd")
     return out, final_state
 
 
@@ -254,27 +251,24 @@ def gtr_ssm_scan_bwd(u, dt, A, Bm, Cm, d_out, Hgrid: int, Wgrid: int, direction:
     grad_init_state) to fill, or None to allocate them (those of absent inputs stay None,
     grad_init_state unless want_init_grad).  Returns that tuple: the activations' gradients of
     their type, the parameters' and the state's float32."""
-    lib = load()
-    m, (B, N, C, S) = _ssm(u, dt, A, Bm, Cm, Hgrid, Wgrid, direction, D, z, dt_bias, dt_softplus, init_state)
-    t, f = u.dtype, torch.float32
-    ld = _rows(d_out, "d_out", (B, N, C), t)
-    _dense(d_final_state, "d_final_state", (B, C, S), f, required=False)
+    m, (B, N, C, S), dev = _ssm(u, dt, A, Bm, Cm, Hgrid, Wgrid, direction, D, z, dt_bias, dt_softplus, init_state)
+    t, f, tok, st = u.dtype, torch.float32, (B, N, C), (B, N, S)
+    ld = _rows(d_out, "d_out", tok, t, dev)
+    df = _dense(d_final_state, "d_final_state", (B, C, S), f, dev, False)
     if grads is None:
-        new = lambda shape, ty: _new(shape, ty, u.device, stream)  # noqa: E731
-        grads = (new((B, N, C), t), new((B, N, C), t), new((C, S), f), new((B, N, S), t), new((B, N, S), t),
-                 None if D is None else new((C,), f), None if z is None else new((B, N, C), t),
-                 None if dt_bias is None else new((C,), f), new((B, C, S), f) if want_init_grad else None)
+        grads = (_new(u, tok, t, stream), _new(u, tok, t, stream), _new(u, (C, S), f, stream), _new(u, st, t, stream),
+                 _new(u, st, t, stream), None if D is None else _new(u, (C,), f, stream),
+                 None if z is None else _new(u, tok, t, stream), None if dt_bias is None else _new(u, (C,), f, stream),
+                 _new(u, (B, C, S), f, stream) if want_init_grad else None)
     gu, gdt, gA, gB, gC, gD, gz, gt, gi = grads
-    for g, name, shape, ty, req in ((gu, "grad_u", (B, N, C), t, True), (gdt, "grad_dt", (B, N, C), t, True),
-                                    (gA, "grad_A", (C, S), f, True), (gB, "grad_Bm", (B, N, S), t, True),
-                                    (gC, "grad_Cm", (B, N, S), t, True), (gD, "grad_D", (C,), f, False),
-                                    (gz, "grad_z", (B, N, C), t, z is not None), (gt, "grad_dt_bias", (C,), f, False),
-                                    (gi, "grad_init_state", (B, C, S), f, False)):
-        _dense(g, name, shape, ty, required=req)
     if z is None and gz is not None:
         raise ValueError("grad_z without z")
-    ws, nbytes = _workspace(workspace, ssm_scan_bwd_workspace_bytes(B, Hgrid, Wgrid, C, S), u.device, stream)
-    g = _SsmGrads(_addr(gu), _addr(gdt), _addr(gB), _addr(gC), _addr(gz), _addr(gA), _addr(gD), _addr(gt), _addr(gi))
-    _check(lib.gtr_ssm_scan_bwd(ctypes.byref(m), _ptr(d_out), ld, _ptr(d_final_state), ctypes.byref(g), _ptr(ws),
-                                nbytes, _stream_handle(stream)), "gtr_ssm_scan_bwd")
+    g = _SsmGrads(_dense(gu, "grad_u", tok, t, dev), _dense(gdt, "grad_dt", tok, t, dev),
+                  _dense(gB, "grad_Bm", st, t, dev), _dense(gC, "grad_Cm", st, t, dev),
+                  _dense(gz, "grad_z", tok, t, dev, z is not None), _dense(gA, "grad_A", (C, S), f, dev),
+                  _dense(gD, "grad_D", (C,), f, dev, False), _dense(gt, "grad_dt_bias", (C,), f, dev, False),
+                  _dense(gi, "grad_init_state", (B, C, S), f, dev, False))
+    ws, wp, nbytes = _workspace(workspace, ssm_scan_bwd_workspace_bytes(B, Hgrid, Wgrid, C, S), u, stream)
+    _check(load().gtr_ssm_scan_bwd(ctypes.byref(m), d_out.data_ptr(), ld, df, ctypes.byref(g), wp, nbytes,
+                                   _stream(stream)), "gtr_ssm_scan_bwd")
     return grads
