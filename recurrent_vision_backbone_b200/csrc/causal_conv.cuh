@@ -9,6 +9,8 @@
 // K is 2 to 4: 2 K operations for 4 bytes moved (6 backward), so HBM-bound.
 #pragma once
 
+#include <type_traits>
+
 namespace gtr {
 namespace cv {
 
@@ -110,141 +112,163 @@ __global__ void __launch_bounds__(kThreads) causal_conv_fwd_kernel(const Args a)
     if (bad) set_error(kOpsErrRange);
 }
 
-// Backward.  A block: 32 channel groups (threadIdx.x) by kLanes position lanes (threadIdx.y);
-// a lane walks `tile` positions and the K - 1 behind them (whose ds its last outputs need),
-// keeping the last K rows of X and of ds in registers and its share of dw and dbias; the lanes'
-// shares meet in shared memory and the block writes one partial row, so that the sum over
-// tokens has a fixed order.  Rows are requested kAhead steps before they are used.
-constexpr int kLanes = 8, kAhead = 4;
-template <typename T, int V, int K>
-__global__ void __launch_bounds__(32 * kLanes) causal_conv_bwd_kernel(const Args a) {
-    __shared__ float red[kLanes][32][V];
+// Backward.  A block: 128 channels, a pair a thread, of a chunk of positions and the K - 1 behind
+// it (whose ds its last outputs need).  A thread walks the chunk with the last K rows of X and of ds
+// in registers and sums its channels' dw and dbias, one partial row a block, so that the sum over
+// tokens has a fixed order.  Rows come in tiles of kTok tokens through shared memory, as 16-byte
+// asynchronous copies two tiles ahead (element by element where rows do not line up), and leave
+// through it as well: with rows read straight into registers the addresses were half of the
+// instructions (114 us at 8 x 2304 tokens of 2048 channels).  A tile inside the chunk and the
+// sequence runs without a branch; the first and the last test every step.
+constexpr int kBwdThreads = 64, kTok = 8, kStages = 3;
+template <typename T, int K, bool WIDE>
+__global__ void __launch_bounds__(kBwdThreads, 8) causal_conv_bwd_kernel(const Args a) {
+    constexpr int CH = 2 * kBwdThreads, RT = CH / 8;   // channels; threads that stage a row
+    constexpr int RP = kTok * RT / kBwdThreads;        // rows of a tile that a thread stages
+    __shared__ __align__(16) uint16_t rows[kStages][2][kTok][CH];
+    __shared__ __align__(16) uint16_t outs[2][kTok][CH];
     chain_wait();
-    const int g = blockIdx.x % ((a.groups + 31) / 32) * 32 + threadIdx.x;
-    const int part = blockIdx.x / ((a.groups + 31) / 32);
-    const long long t = (long long)part * kLanes + threadIdx.y;
-    const int b = (int)(t / a.tiles);
-    const bool live = g < a.groups && b < a.B;
-    const int c = g * V;
-    float acc[K + 1][V];
+    const int tid = threadIdx.x, cb = blockIdx.x % a.groups, part = blockIdx.x / a.groups;
+    const int b = part / a.tiles, chunk = part - b * a.tiles;
+    const int p0 = chunk * a.tile;
+    const int own = min(a.tile, a.N - p0), steps = own + K - 1;   // steps n: position p0 + n
+    const bool tail = p0 + steps > a.N;                           // some steps lie behind the sequence
+    const long long row0 = (long long)b * a.N;
+    const int c = cb * CH + 2 * tid;
+    const bool v0 = c < a.D, v1 = c + 1 < a.D;
+
+    // staging: this thread's rows tt + (kTok / RP) r of a tile, 8 channels of them
+    constexpr int RS = kTok / RP;
+    const int tt = tid / RT, tc = tid % RT, c8 = cb * CH + tc * 8, left = a.D - c8;
+    Walk in0(min(p0 + tt, a.N - 1), a.H, a.W, a.dir);
+    static_assert(RP == 2, "two rows of a tile a thread");
+    Walk in1(min(p0 + tt + RS, a.N - 1), a.H, a.W, a.dir);
+    auto stage = [&](int n0, int s) {
 #pragma unroll
-    for (int j = 0; j <= K; ++j)
-#pragma unroll
-        for (int v = 0; v < V; ++v) acc[j][v] = 0.f;
+        for (int r = 0; r < RP; ++r) {
+            const int n = n0 + tt + RS * r;
+            const bool in = n < steps && p0 + n < a.N;
+            const long long row = row0 + (in ? (r ? in1.n : in0.n) : 0);
+            stage_row<WIDE>(&rows[s][0][tt + RS * r][tc * 8], a.x + row * a.ldx + c8, in, left);
+            stage_row<WIDE>(&rows[s][1][tt + RS * r][tc * 8], a.dy + row * a.lddy + c8, in, left);
+        }
+        in0.advance(kTok);
+        in1.advance(kTok);
+        if (WIDE) copy_commit();
+    };
+    stage(0, 0);
+    stage(kTok, 1);
+
+    // rows leave as they came: row p = p0 + n of dX is position p - (K - 1), or an earlier input
     bool bad = false;
-    if (live) {
-        const int tile = (int)(t - (long long)b * a.tiles), p0 = tile * a.tile;
-        const int p1 = min(p0 + a.tile, a.N);            // own positions: p0 .. p1 - 1
-        const int pe = p1 + K - 1;                       // rows of dX reached at steps p0 .. pe - 1
-        const long long row0 = (long long)b * a.N;
-        float w[V][K], bias[V];
+    Walk out0(max(p0 + tt - (K - 1), 0), a.H, a.W, a.dir), out1(max(p0 + tt + RS - (K - 1), 0), a.H, a.W, a.dir);
+    auto flush = [&](int n0, int buf) {
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
+        for (int r = 0; r < RP; ++r) {
+            const int n = n0 + tt + RS * r, p = p0 + n;
+            const bool out = n >= K - 1;
+            uint16_t *dst = out ? a.dx + (row0 + (r ? out1.n : out0.n)) * a.D + c8
+                                : a.dinit != nullptr && p < K - 1 ? a.dinit + ((long long)b * (K - 1) + p) * a.D + c8 : nullptr;
+            if (n < steps && left > 0 && dst != nullptr) {
+                const Raw<8> v = load_raw_shared<8>(&outs[buf][tt + RS * r][tc * 8]);
+                if (WIDE) {
 #pragma unroll
-            for (int j = 0; j < K; ++j) w[v][j] = __ldg(a.w + (long long)(c + v) * K + j);
-            bias[v] = a.bias != nullptr ? __ldg(a.bias + c + v) : 0.f;
-        }
-        float xw[K][V], dw[K][V];   // rows p .. p + K - 1 of X; ds of positions p - K + 1 .. p
+                    for (const uint32_t w : v.w) bad |= Elem<T>::bad_raw(w);
+                    store_raw<8>(dst, v);
+                } else {
 #pragma unroll
-        for (int r = 0; r < K - 1; ++r) {
-            const int p = p0 - (K - 1) + r;
-            unpack<T, V>(p >= 0 ? load_raw<V>(a.x + (row0 + token_of(p, a.H, a.W, a.dir)) * a.ldx + c)
-                                : early_row<V>(a, b, r, K, c), xw[r]);
-        }
-#pragma unroll
-        for (int j = 0; j < K; ++j)
-#pragma unroll
-            for (int v = 0; v < V; ++v) dw[j][v] = 0.f;
-        Walk ahead(p0, a.H, a.W, a.dir), behind(max(p0 - (K - 1), 0), a.H, a.W, a.dir);
-        Raw<V> qx[kAhead], qd[kAhead];
-        auto fetch = [&](int p, int i) {
-            const bool in = p < a.N && p < pe;
-            qx[i] = in ? load_raw<V>(a.x + (row0 + ahead.n) * a.ldx + c) : zero_raw<V>();
-            qd[i] = in ? load_raw<V>(a.dy + (row0 + ahead.n) * a.lddy + c) : zero_raw<V>();
-            ahead.next();
-        };
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i) fetch(p0 + i, i);
-        for (int pb = p0; pb < pe; pb += kAhead) {
-#pragma unroll
-            for (int i = 0; i < kAhead; ++i) {
-                const int p = pb + i;
-                if (p >= pe) break;
-                float dy[V];
-                unpack<T, V>(qx[i], xw[K - 1]);
-                unpack<T, V>(qd[i], dy);
-                fetch(p + kAhead, i);
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    float d = dy[v];
-                    if (a.act == GTR_ACT_SILU) {
-                        float s = bias[v];
-#pragma unroll
-                        for (int j = 0; j < K; ++j) s = fmaf(w[v][j], xw[j][v], s);
-                        const float sg = sigmoid_f(s);
-                        d *= sg * fmaf(s, 1.f - sg, 1.f);
-                    }
-                    // behind the sequence there is no ds (not 0 times what the activation makes of X)
-                    dw[K - 1][v] = p < a.N ? d : 0.f;
+                    for (int i = 0; i < 8; ++i)
+                        if (i < left) {
+                            const uint16_t q = (uint16_t)(i & 1 ? v.w[i / 2] >> 16 : v.w[i / 2]);
+                            bad |= Elem<T>::bad_raw(q);
+                            dst[i] = q;
+                        }
                 }
-                if (p < p1) {
-#pragma unroll
-                    for (int v = 0; v < V; ++v) {
-#pragma unroll
-                        for (int j = 0; j < K; ++j) acc[j][v] = fmaf(dw[K - 1][v], xw[j][v], acc[j][v]);
-                        acc[K][v] += dw[K - 1][v];
-                    }
-                }
-                // row p of dX: position p - (K - 1), or an earlier input where p < K - 1
-                const bool own = p >= p0 + K - 1, first = p0 == 0 && p < K - 1;
-                if (own || (first && a.dinit != nullptr)) {
-                    float e[V];
-#pragma unroll
-                    for (int v = 0; v < V; ++v) {
-                        e[v] = 0.f;
-#pragma unroll
-                        for (int j = 0; j < K; ++j) e[v] = fmaf(w[v][j], dw[K - 1 - j][v], e[v]);
-                    }
-                    if (a.dfin != nullptr && p >= a.N) {
-                        float f[V];
-                        unpack<T, V>(load_raw<V>(a.dfin + ((long long)b * (K - 1) + p - a.N) * a.D + c), f);
-#pragma unroll
-                        for (int v = 0; v < V; ++v) e[v] += f[v];
-                    }
-#pragma unroll
-                    for (int v = 0; v < V; ++v) bad |= Elem<T>::bad(e[v]);
-                    if (own)
-                        store_raw<V>(a.dx + (row0 + behind.n) * a.D + c, pack<T, V>(e));
-                    else
-                        store_raw<V>(a.dinit + ((long long)b * (K - 1) + p) * a.D + c, pack<T, V>(e));
-                }
-                if (p >= K - 1) behind.next();
-#pragma unroll
-                for (int j = 0; j < K - 1; ++j)
-#pragma unroll
-                    for (int v = 0; v < V; ++v) {
-                        xw[j][v] = xw[j + 1][v];
-                        dw[j][v] = dw[j + 1][v];
-                    }
             }
+            // the next tile's row; a row ahead of the sequence (an earlier input) is followed by kTok - the rest
+            Walk &w = r ? out1 : out0;
+            const int q = p - (K - 1);
+            w.advance(q < 0 ? kTok + q : kTok);
         }
+    };
+
+    float2 w[K], acc[K + 1];
+    auto param = [&](const float *p, int j, int st) {
+        return make_float2(p != nullptr && v0 ? __ldg(p + (long long)c * st + j) : 0.f,
+                           p != nullptr && v1 ? __ldg(p + (long long)(c + 1) * st + j) : 0.f);
+    };
+#pragma unroll
+    for (int j = 0; j < K; ++j) w[j] = param(a.w, j, K);
+    const float2 bias = param(a.bias, 0, 1);
+#pragma unroll
+    for (int j = 0; j <= K; ++j) acc[j] = splat(0.f);
+    float2 xw[K], dw[K];   // rows p .. p + K - 1 of X; ds of positions p - K + 1 .. p
+#pragma unroll
+    for (int r = 0; r < K - 1; ++r) {
+        const int p = p0 - (K - 1) + r;
+        const uint16_t *src = p >= 0 ? a.x + (row0 + token_of(p, a.H, a.W, a.dir)) * a.ldx + c
+                                     : a.init != nullptr ? a.init + ((long long)b * (K - 1) + r) * a.D + c : nullptr;
+        xw[r] = make_float2(src != nullptr && v0 ? Elem<T>::get(__ldg(src)) : 0.f,
+                            src != nullptr && v1 ? Elem<T>::get(__ldg(src + 1)) : 0.f);
     }
+#pragma unroll
+    for (int j = 0; j < K; ++j) dw[j] = splat(0.f);
+
+    const bool silu = a.act == GTR_ACT_SILU;
+    auto tile = [&](auto full, int n0, int s, int buf) {
+        constexpr bool FULL = decltype(full)::value;   // every step the block's own and inside the sequence
+#pragma unroll
+        for (int i = 0; i < kTok; ++i) {
+            const int n = n0 + i;
+            if (!FULL && n >= steps) break;
+            xw[K - 1] = Elem<T>::get2(*reinterpret_cast<const uint32_t *>(&rows[s][0][i][2 * tid]));
+            const float2 dy = Elem<T>::get2(*reinterpret_cast<const uint32_t *>(&rows[s][1][i][2 * tid]));
+            float2 z = bias;
+#pragma unroll
+            for (int j = 0; j < K; ++j) z = __ffma2_rn(w[j], xw[j], z);
+            const float2 sg = make_float2(sigmoid_f(z.x), sigmoid_f(z.y));
+            const float2 one = __ffma2_rn(z, __fadd2_rn(splat(1.f), make_float2(-sg.x, -sg.y)), splat(1.f));
+            const float2 d = __fmul2_rn(dy, __fmul2_rn(sg, one));
+            dw[K - 1] = make_float2(silu ? d.x : dy.x, silu ? d.y : dy.y);
+            // behind the sequence there is no ds (not 0 times what the activation makes of X)
+            if (!FULL && p0 + n >= a.N) dw[K - 1] = splat(0.f);
+            if (FULL || n < own) {
+#pragma unroll
+                for (int j = 0; j < K; ++j) acc[j] = __ffma2_rn(dw[K - 1], xw[j], acc[j]);
+                acc[K] = __fadd2_rn(acc[K], dw[K - 1]);
+            }
+            float2 e = __fmul2_rn(w[0], dw[K - 1]);
+#pragma unroll
+            for (int j = 1; j < K; ++j) e = __ffma2_rn(w[j], dw[K - 1 - j], e);
+            if (!FULL && a.dfin != nullptr && p0 + n >= a.N) {
+                const uint16_t *f = a.dfin + ((long long)b * (K - 1) + p0 + n - a.N) * a.D + c;
+                e = __fadd2_rn(e, make_float2(v0 ? Elem<T>::get(__ldg(f)) : 0.f, v1 ? Elem<T>::get(__ldg(f + 1)) : 0.f));
+            }
+            *reinterpret_cast<uint32_t *>(&outs[buf][i][2 * tid]) = Elem<T>::put2(e.x, e.y);
+#pragma unroll
+            for (int j = 0; j < K - 1; ++j) xw[j] = xw[j + 1], dw[j] = dw[j + 1];
+        }
+    };
+    int s = 0, buf = 0;
+    for (int n0 = 0; n0 < steps; n0 += kTok, buf ^= 1) {
+        if (WIDE) copy_wait<kStages - 2>();
+        __syncthreads();   // this tile's rows are here, the tile before has been computed
+        stage(n0 + (kStages - 1) * kTok, s == 0 ? kStages - 1 : s - 1);
+        if (n0 > 0) flush(n0 - kTok, buf ^ 1);
+        if (n0 + kTok <= own && !(tail && p0 + n0 + kTok > a.N))
+            tile(std::true_type{}, n0, s, buf);
+        else
+            tile(std::false_type{}, n0, s, buf);
+        s = s == kStages - 1 ? 0 : s + 1;
+    }
+    __syncthreads();
+    flush((steps - 1) / kTok * kTok, buf ^ 1);
     if (bad) set_error(kOpsErrRange);
 #pragma unroll
     for (int j = 0; j <= K; ++j) {
-        __syncthreads();
-#pragma unroll
-        for (int v = 0; v < V; ++v) red[threadIdx.y][threadIdx.x][v] = acc[j][v];
-        __syncthreads();
-        for (int i = threadIdx.y * 32 + threadIdx.x; i < 32 * V; i += 32 * kLanes) {
-            const int ch = (blockIdx.x % ((a.groups + 31) / 32)) * 32 * V + i;
-            if (ch < a.D) {
-                float s = 0.f;
-#pragma unroll
-                for (int l = 0; l < kLanes; ++l) s += red[l][i / V][i % V];
-                a.part[((long long)part * (K + 1) + j) * a.D + ch] = s;
-            }
-        }
+        float *dst = a.part + ((long long)part * (K + 1) + j) * a.D + c;
+        if (v0) dst[0] = acc[j].x;
+        if (v1) dst[1] = acc[j].y;
     }
 }
 

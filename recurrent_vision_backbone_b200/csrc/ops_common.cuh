@@ -152,6 +152,22 @@ __device__ __forceinline__ void copy_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+__device__ __forceinline__ uint16_t ld16(const uint16_t *p, bool in) { return in ? __ldg(p) : (uint16_t)0; }
+// Eight channels of a row to shared memory, `left` of them inside the tensor; zeros where !in.  WIDE:
+// an asynchronous 16-byte copy (rows on 16 bytes, whole pieces); else element by element.
+template <bool WIDE>
+__device__ __forceinline__ void stage_row(uint16_t *dst, const uint16_t *src, bool in, int left) {
+    if constexpr (WIDE) {
+        copy16_async(dst, src, in && left > 0 ? 16u : 0u);   // 0 bytes: zeros
+    } else {
+        Raw<8> r;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            r.w[i] = (uint32_t)ld16(src + 2 * i, in && 2 * i < left) | (uint32_t)ld16(src + 2 * i + 1, in && 2 * i + 1 < left) << 16;
+        store_raw<8>(dst, r);
+    }
+}
+
 // ------------------------------------------------------------------ functions
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;

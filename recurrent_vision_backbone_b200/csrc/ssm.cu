@@ -53,22 +53,22 @@ constexpr long long kMaxGrid = 0x7fffffffLL;
 
 // ------------------------------------------------------------------ convolution
 struct ConvPlan {
-    long long tiles;    // per sequence
-    long long parts;    // blocks along the positions
-    int tile;
+    long long tiles;    // chunks of a sequence
+    long long parts;    // chunks
+    int tile;           // positions of a chunk
 };
-// Backward: 16 positions a lane at least (each lane recomputes K - 1 more), more once the
-// blocks pass four an SM: every block writes a partial row of the parameters' sums.
+// Backward: chunks enough for one wave of eight blocks an SM (every block writes a partial row of the
+// parameters' sums), of 32 positions at least (each recomputes K - 1 more).
 static ConvPlan conv_bwd_plan(int B, long long N, int D) {
     ConvPlan p{};
-    const long long blocks_c = (D + 63) / 64, want = 148 * 4;
-    long long tile = ((long long)B * N * blocks_c + want * cv::kLanes - 1) / (want * cv::kLanes);
-    if (tile < 16) tile = 16;
-    if (tile > N) tile = N;
-    if (tile < 4) tile = 4;
+    const long long blocks_c = (D + 127) / 128;
+    long long tiles = 148 * 8 / (blocks_c * B);
+    if (tiles < 1) tiles = 1;
+    long long tile = (N + tiles - 1) / tiles;
+    if (tile < 32) tile = 32;
     p.tile = (int)tile;
     p.tiles = (N + tile - 1) / tile;
-    p.parts = ((long long)B * p.tiles + cv::kLanes - 1) / cv::kLanes;
+    p.parts = (long long)B * p.tiles;
     return p;
 }
 
@@ -128,23 +128,24 @@ static cudaError_t conv_fwd_k(const cv::Args &a, int K, cudaStream_t s) {
     }
 }
 
-template <typename T, int V, int K>
-static cudaError_t conv_bwd_launch(cv::Args a, const ConvPlan &p, float *gw, float *gb, cudaStream_t s) {
-    a.groups = (a.D + V - 1) / V;
-    const long long blocks = p.parts * ((a.groups + 31) / 32);
+template <typename T, int K>
+static cudaError_t conv_bwd_launch(cv::Args a, const ConvPlan &p, bool wide, float *gw, float *gb, cudaStream_t s) {
+    a.groups = (a.D + 2 * cv::kBwdThreads - 1) / (2 * cv::kBwdThreads);
+    const long long blocks = p.parts * a.groups;
     if (blocks > kMaxGrid) return cudaErrorInvalidConfiguration;
-    const cudaError_t e = launch_after(cv::causal_conv_bwd_kernel<T, V, K>, (unsigned)blocks, dim3(32, cv::kLanes), 0, s, a);
+    const cudaError_t e = launch_after(wide ? cv::causal_conv_bwd_kernel<T, K, true> : cv::causal_conv_bwd_kernel<T, K, false>,
+                                       (unsigned)blocks, dim3(cv::kBwdThreads), 0, s, a);
     if (e != cudaSuccess) return e;
     const long long cols = (long long)(K + 1) * a.D;
     return launch_after(cv::causal_conv_sum_kernel<K>, (unsigned)((cols + 31) / 32), dim3(32, 8), 0, s,
                         (const float *)a.part, (int)p.parts, a.D, gw, gb);
 }
-template <typename T, int V>
-static cudaError_t conv_bwd_k(const cv::Args &a, int K, const ConvPlan &p, float *gw, float *gb, cudaStream_t s) {
+template <typename T>
+static cudaError_t conv_bwd_k(const cv::Args &a, int K, const ConvPlan &p, bool wide, float *gw, float *gb, cudaStream_t s) {
     switch (K) {
-    case 2: return conv_bwd_launch<T, V, 2>(a, p, gw, gb, s);
-    case 3: return conv_bwd_launch<T, V, 3>(a, p, gw, gb, s);
-    default: return conv_bwd_launch<T, V, 4>(a, p, gw, gb, s);
+    case 2: return conv_bwd_launch<T, 2>(a, p, wide, gw, gb, s);
+    case 3: return conv_bwd_launch<T, 3>(a, p, wide, gw, gb, s);
+    default: return conv_bwd_launch<T, 4>(a, p, wide, gw, gb, s);
     }
 }
 
@@ -438,15 +439,9 @@ extern "C" gtr_status_t gtr_causal_conv_bwd(const gtr_conv_t *conv, const void *
     a.tiles = (int)p.tiles;
     const void *ps[] = {a.x, a.init, a.dy, a.dfin, a.dx, a.dinit};
     const long long lds[] = {a.ldx, a.lddy};
-    // pairs of channels where the rows line up to 4 bytes: a warp reads whole 128-byte lines and
-    // the sliding windows of a pair fit the registers
-    const bool wide = rows_on(4, a.D, ps, 6, lds, 2);
-    const bool h = conv->dtype == GTR_F16;
-    return ops_cuda_status(
-        wide ? (h ? conv_bwd_k<__half, 2>(a, conv->K, p, grad_w, grad_bias, s)
-                  : conv_bwd_k<__nv_bfloat16, 2>(a, conv->K, p, grad_w, grad_bias, s))
-             : (h ? conv_bwd_k<__half, 1>(a, conv->K, p, grad_w, grad_bias, s)
-                  : conv_bwd_k<__nv_bfloat16, 1>(a, conv->K, p, grad_w, grad_bias, s)));
+    const bool wide = rows_on(16, a.D, ps, 6, lds, 2);
+    return ops_cuda_status(conv->dtype == GTR_F16 ? conv_bwd_k<__half>(a, conv->K, p, wide, grad_w, grad_bias, s)
+                                                  : conv_bwd_k<__nv_bfloat16>(a, conv->K, p, wide, grad_w, grad_bias, s));
 }
 
 extern "C" size_t gtr_ssm_scan_fwd_workspace_bytes(int B, int Hgrid, int Wgrid, int D, int S) {

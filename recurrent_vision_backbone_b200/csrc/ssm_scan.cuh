@@ -50,7 +50,6 @@ struct Args {
     float *pbc, *pd, *pt;           // workspace: [tiles][B N][2 SP], [B P][D], [B P][D]
 };
 
-__device__ __forceinline__ uint16_t ld16(const uint16_t *p, bool in) { return in ? __ldg(p) : (uint16_t)0; }
 
 enum { kLocal = 0, kOut = 1, kLocalBwd = 2 };
 
@@ -75,20 +74,6 @@ __device__ __forceinline__ int butterfly(float *v, int lane) {
     }
 }
 __host__ __device__ constexpr int left_of(int nv, int lanes) { return nv > lanes ? nv / lanes : 1; }
-
-// Rows of one tensor that a walk stages: the thread's 8 channels of its token.
-template <bool WIDE>
-__device__ __forceinline__ void stage_row(uint16_t *dst, const uint16_t *src, bool in, int left) {
-    if constexpr (WIDE) {
-        copy16_async(dst, src, in && left > 0 ? 16u : 0u);   // 0 bytes: zeros
-    } else {
-        Raw<8> r;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            r.w[i] = (uint32_t)ld16(src + 2 * i, in && 2 * i < left) | (uint32_t)ld16(src + 2 * i + 1, in && 2 * i + 1 < left) << 16;
-        store_raw<8>(dst, r);
-    }
-}
 
 template <int MODE>
 __host__ __device__ constexpr int walk_rows() { return MODE == kLocal ? 2 : MODE == kOut ? 3 : 4; }
