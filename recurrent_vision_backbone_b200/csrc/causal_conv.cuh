@@ -43,13 +43,11 @@ __device__ __forceinline__ Raw<V> early_row(const Args &a, int b, int r, int K, 
 template <typename T, int V, int K, int TP>
 __global__ void __launch_bounds__(kThreads) causal_conv_fwd_kernel(const Args a) {
     chain_wait();
-    const long long id = (long long)blockIdx.x * kThreads + threadIdx.x;
-    const int g = (int)(id % a.groups);
-    const long long t = id / a.groups;
-    const int b = (int)(t / a.tiles);
+    long long g, tile;
+    const long long t = div_rem((long long)blockIdx.x * kThreads + threadIdx.x, a.groups, g);
+    const int b = (int)div_rem(t, a.tiles, tile);
     if (b >= a.B) return;
-    const int tile = (int)(t - (long long)b * a.tiles);
-    const int c = g * V, p0 = tile * TP;
+    const int c = (int)g * V, p0 = (int)tile * TP;
     const long long row0 = (long long)b * a.N;
     Raw<V> x[TP + K - 1];
     int tok[TP];
@@ -67,6 +65,25 @@ __global__ void __launch_bounds__(kThreads) causal_conv_fwd_kernel(const Args a)
             wk.next();
         }
     }
+    // the weights of V channels lie together: V K floats, in 16-byte pieces where they can be
+    float w[V][K], bias[V];
+    if constexpr (V % 4 == 0) {
+        float4 q[V * K / 4];
+#pragma unroll
+        for (int i = 0; i < V * K / 4; ++i) q[i] = __ldg(reinterpret_cast<const float4 *>(a.w + (long long)c * K) + i);
+#pragma unroll
+        for (int i = 0; i < V * K; ++i) {
+            const float4 f = q[i / 4];
+            w[i / K][i % K] = i % 4 == 0 ? f.x : i % 4 == 1 ? f.y : i % 4 == 2 ? f.z : f.w;
+        }
+    } else {
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+#pragma unroll
+            for (int j = 0; j < K; ++j) w[v][j] = __ldg(a.w + (long long)(c + v) * K + j);
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) bias[v] = a.bias != nullptr ? __ldg(a.bias + c + v) : 0.f;
     // tile 0 also writes the carried rows: the last K - 1 of X.  The rows it needs of
     // init_state are in registers by then, so final_state may be init_state
     if (tile == 0 && a.fin != nullptr) {
@@ -79,13 +96,6 @@ __global__ void __launch_bounds__(kThreads) causal_conv_fwd_kernel(const Args a)
         }
 #pragma unroll
         for (int j = 0; j < K - 1; ++j) store_raw<V>(a.fin + ((long long)b * (K - 1) + j) * a.D + c, f[j]);
-    }
-    float w[V][K], bias[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-#pragma unroll
-        for (int j = 0; j < K; ++j) w[v][j] = __ldg(a.w + (long long)(c + v) * K + j);
-        bias[v] = a.bias != nullptr ? __ldg(a.bias + c + v) : 0.f;
     }
     float win[K][V];
 #pragma unroll
@@ -172,8 +182,7 @@ __global__ void __launch_bounds__(kBwdThreads, 8) causal_conv_bwd_kernel(const A
             if (n < steps && left > 0 && dst != nullptr) {
                 const Raw<8> v = load_raw_shared<8>(&outs[buf][tt + RS * r][tc * 8]);
                 if (WIDE) {
-#pragma unroll
-                    for (const uint32_t w : v.w) bad |= Elem<T>::bad_raw(w);
+                    bad |= Elem<T>::bad_raw(Elem<T>::worst(Elem<T>::worst(v.w[0], v.w[1]), Elem<T>::worst(v.w[2], v.w[3])));
                     store_raw<8>(dst, v);
                 } else {
 #pragma unroll

@@ -51,6 +51,11 @@ struct Elem<__half> {
     static __device__ __forceinline__ bool bad_raw(uint32_t w) {
         return (w & 0x7c00u) == 0x7c00u || (w & 0x7c000000u) == 0x7c000000u;
     }
+    // the larger magnitudes of two pairs (a NaN wins), to be tested once
+    static __device__ __forceinline__ uint32_t worst(uint32_t a, uint32_t b) {
+        const __half2 m = __hmax2_nan(*reinterpret_cast<const __half2 *>(&a), __habs2(*reinterpret_cast<const __half2 *>(&b)));
+        return *reinterpret_cast<const uint32_t *>(&m);
+    }
 };
 template <>
 struct Elem<__nv_bfloat16> {
@@ -65,6 +70,7 @@ struct Elem<__nv_bfloat16> {
     }
     static __device__ __forceinline__ bool bad(float) { return false; }   // bf16 holds what float32 holds
     static __device__ __forceinline__ bool bad_raw(uint32_t) { return false; }
+    static __device__ __forceinline__ uint32_t worst(uint32_t, uint32_t) { return 0; }
 };
 
 // V consecutive elements as raw words: V = 8 is one 16-byte access, 4 an 8-byte one, 2 a
@@ -225,6 +231,41 @@ __device__ __forceinline__ float sigmoid_of(float x, float e) {
 }
 __device__ __forceinline__ float softplus_f(float x) {
     return fmaxf(x, 0.f) + log1p_01(ex2(fabsf(x) * -kLog2e));
+}
+
+// ------------------------------------------------------------------ sums over lanes
+// Sums over lanes whose index differs in the bits [LO, HI): v[0 .. NV - 1] of every lane.  While
+// a lane holds several values a round exchanges half of them; then whole values.  Lane l ends
+// with the sums of the values [idx, idx + left) in v[0 .. left - 1], where idx is returned.
+template <int LO, int HI, int NV>
+__device__ __forceinline__ int butterfly(float *v, int lane) {
+    if constexpr (LO >= HI) {
+        return 0;
+    } else if constexpr (NV > 1) {
+        const bool up = lane & LO;
+#pragma unroll
+        for (int i = 0; i < NV / 2; ++i) {
+            const float send = up ? v[i] : v[i + NV / 2], keep = up ? v[i + NV / 2] : v[i];
+            v[i] = keep + __shfl_xor_sync(0xffffffffu, send, LO);
+        }
+        return (up ? NV / 2 : 0) + butterfly<LO * 2, HI, NV / 2>(v, lane);
+    } else {
+        v[0] += __shfl_xor_sync(0xffffffffu, v[0], LO);
+        return butterfly<LO * 2, HI, 1>(v, lane);
+    }
+}
+
+// n / d with the remainder in r, n >= 0, d > 0: a 32-bit division wherever that will do (a 64-bit one
+// takes several times as long, and what follows waits for it).
+__device__ __forceinline__ long long div_rem(long long n, long long d, long long &r) {
+    if (((n | d) >> 32) == 0) {
+        const uint32_t q = (uint32_t)n / (uint32_t)d;
+        r = (uint32_t)n - q * (uint32_t)d;
+        return q;
+    }
+    const long long q = n / d;
+    r = n - q * d;
+    return q;
 }
 
 // ------------------------------------------------------------------ launches in a chain

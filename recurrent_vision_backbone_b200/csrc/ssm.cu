@@ -121,10 +121,12 @@ static cudaError_t conv_fwd_launch(cv::Args a, cudaStream_t s) {
 }
 template <typename T, int V>
 static cudaError_t conv_fwd_k(const cv::Args &a, int K, cudaStream_t s) {
+    // four positions a thread instead of eight while eight make fewer than three blocks an SM
+    const bool few = (long long)a.B * ((a.N + 7) / 8) * ((a.D + V - 1) / V) < 148LL * 3 * cv::kThreads;
     switch (K) {
-    case 2: return conv_fwd_launch<T, V, 2, 8>(a, s);
-    case 3: return conv_fwd_launch<T, V, 3, 8>(a, s);
-    default: return conv_fwd_launch<T, V, 4, 8>(a, s);
+    case 2: return few ? conv_fwd_launch<T, V, 2, 4>(a, s) : conv_fwd_launch<T, V, 2, 8>(a, s);
+    case 3: return few ? conv_fwd_launch<T, V, 3, 4>(a, s) : conv_fwd_launch<T, V, 3, 8>(a, s);
+    default: return few ? conv_fwd_launch<T, V, 4, 4>(a, s) : conv_fwd_launch<T, V, 4, 8>(a, s);
     }
 }
 
@@ -305,10 +307,17 @@ static cudaError_t scan_fwd_launch(const sc::Args &a, int sl, bool wide, cudaStr
     o.tiles = (a.D * (long long)sl + sc::kThreads - 1) / sc::kThreads;
     return sl == 1 ? walk_launch<T, SP, sc::kOut, 1>(o, wide, s) : walk_launch<T, SP, sc::kOut, 2>(o, wide, s);
 }
+template <typename T, int S, int NB>
+static cudaError_t token_launch_nb(const sc::Args &a, cudaStream_t s) {
+    const long long n = ((long long)a.B + NB - 1) / NB * a.D * (S / 4);
+    const bool bcw = aligned_to(a.bm, 8) && aligned_to(a.cm, 8) && (a.B == 1 || (a.ldb % 4 == 0 && a.ldc % 4 == 0));
+    return launch_after(bcw ? sc::ssm_token_kernel<T, S, NB, true> : sc::ssm_token_kernel<T, S, NB, false>,
+                        (unsigned)((n + 255) / 256), dim3(256), 0, s, a);
+}
+// As many sequences a thread as lanes share a channel, once that leaves every SM eight blocks or more.
 template <typename T, int S>
 static cudaError_t token_launch(const sc::Args &a, cudaStream_t s) {
-    const long long n = (long long)a.B * a.D * (S / 4);
-    return launch_after(sc::ssm_token_kernel<T, S>, (unsigned)((n + 255) / 256), dim3(256), 0, s, a);
+    return (long long)a.B * a.D / 256 >= 148 * 8 ? token_launch_nb<T, S, S / 4>(a, s) : token_launch_nb<T, S, 1>(a, s);
 }
 template <typename T>
 static cudaError_t scan_fwd_dispatch(const sc::Args &a, int sl, bool wide, cudaStream_t s) {

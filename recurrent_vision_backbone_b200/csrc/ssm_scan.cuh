@@ -53,26 +53,6 @@ struct Args {
 
 enum { kLocal = 0, kOut = 1, kLocalBwd = 2 };
 
-// Sums over lanes whose index differs in the bits [LO, HI): v[0 .. NV - 1] of every lane.  While
-// a lane holds several values a round exchanges half of them; then whole values.  Lane l ends
-// with the sums of the values [idx, idx + left) in v[0 .. left - 1], where idx is returned.
-template <int LO, int HI, int NV>
-__device__ __forceinline__ int butterfly(float *v, int lane) {
-    if constexpr (LO >= HI) {
-        return 0;
-    } else if constexpr (NV > 1) {
-        const bool up = lane & LO;
-#pragma unroll
-        for (int i = 0; i < NV / 2; ++i) {
-            const float send = up ? v[i] : v[i + NV / 2], keep = up ? v[i + NV / 2] : v[i];
-            v[i] = keep + __shfl_xor_sync(0xffffffffu, send, LO);
-        }
-        return (up ? NV / 2 : 0) + butterfly<LO * 2, HI, NV / 2>(v, lane);
-    } else {
-        v[0] += __shfl_xor_sync(0xffffffffu, v[0], LO);
-        return butterfly<LO * 2, HI, 1>(v, lane);
-    }
-}
 __host__ __device__ constexpr int left_of(int nv, int lanes) { return nv > lanes ? nv / lanes : 1; }
 
 template <int MODE>
@@ -152,7 +132,7 @@ __global__ void __launch_bounds__(kThreads, walk_blocks<SP, MODE, SL>()) ssm_wal
         const Raw<8> r = load_raw_shared<8>(&outs[buf][MODE == kOut ? tt : 0][MODE == kOut ? tc * 8 : 0]);
         uint16_t *dst = a.out + (row0 + n) * a.D + c8;
         if (WIDE) {   // whole pieces
-            bad |= Elem<T>::bad_raw(r.w[0]) | Elem<T>::bad_raw(r.w[1]) | Elem<T>::bad_raw(r.w[2]) | Elem<T>::bad_raw(r.w[3]);
+            bad |= Elem<T>::bad_raw(Elem<T>::worst(Elem<T>::worst(r.w[0], r.w[1]), Elem<T>::worst(r.w[2], r.w[3])));
             store_raw<8>(dst, r);
         } else {
 #pragma unroll
@@ -356,12 +336,10 @@ template <int SP, bool BWD>
 __global__ void __launch_bounds__(kFoldThreads) ssm_fold_kernel(const Args a) {
     chain_wait();
     const long long per = (long long)a.D * SP;
-    const long long id = (long long)blockIdx.x * kFoldThreads + threadIdx.x;
-    const int way = BWD ? (int)(id / (per * a.B)) : 0;   // backward: the states, then the gradients
-    const long long rest = id - way * per * a.B;
-    const int b = (int)(rest / per);
-    if (b >= a.B || way > 1) return;
-    const long long e = rest - b * per;
+    long long e;
+    int b = (int)div_rem((long long)blockIdx.x * kFoldThreads + threadIdx.x, per, e), way = 0;
+    if (BWD && b >= a.B) way = 1, b -= a.B;   // backward: the states, then the gradients
+    if (b >= a.B) return;
     const int d = (int)(e / SP), n = (int)(e % SP);
     const bool in = n < a.S;
     const float A2 = in ? __ldg(a.A + (long long)d * a.S + n) * kLog2e : 0.f;
@@ -380,42 +358,69 @@ __global__ void __launch_bounds__(kFoldThreads) ssm_fold_kernel(const Args a) {
 
 // One token of every sequence: the states are the traffic (read and written once, 8 bytes a
 // state against 8 bytes a channel), so lanes run along a channel's states, 16 bytes each: a
-// warp reads and writes whole lines.  S / 4 lanes a channel (S = 4, 8, 16 or 32).
-template <typename T, int S>
-__global__ void __launch_bounds__(256) ssm_token_kernel(const Args a) {
+// warp reads and writes whole lines.  S / 4 lanes a channel (S = 4, 8, 16 or 32).  A thread takes NB
+// neighbouring sequences, one or as many as lanes share the channel, whose states it asks for at once;
+// each lane then prepares and finishes one of them.  BCW: B and C rows start on 8 bytes.
+template <typename T, int S, int NB, bool BCW>
+__global__ void __launch_bounds__(256, NB <= 4 ? 4 : 2) ssm_token_kernel(const Args a) {
     constexpr int SL = S / 4;
+    static_assert(NB == 1 || NB == SL, "a lane prepares one sequence");
     chain_wait();
     const long long id = (long long)blockIdx.x * 256 + threadIdx.x;
-    const int q = (int)(id % SL);
-    const long long ch = id / SL;
-    const bool live = ch < (long long)a.B * a.D;
-    const int b = live ? (int)(ch / a.D) : 0, c = live ? (int)(ch - (long long)b * a.D) : 0;
-    float4 h = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (live && a.h0 != nullptr) h = *reinterpret_cast<const float4 *>(a.h0 + ch * S + q * 4);
-    const float4 A = __ldg(reinterpret_cast<const float4 *>(a.A + (long long)c * S + q * 4));
-    const float u = Elem<T>::get(__ldg(a.u + b * a.ldu + c));
-    const float raw = Elem<T>::get(__ldg(a.dt + b * a.lddt + c)) + (a.dtb != nullptr ? __ldg(a.dtb + c) : 0.f);
-    float Bv[4], Cv[4];
+    const int q = (int)(id % SL), lane = threadIdx.x & 31;
+    long long cc;
+    const long long bg = div_rem(id / SL, a.D, cc);
+    const int c = (int)cc;
+    const long long b0 = bg * NB;
+    // the sequence this lane prepares: the one whose sum butterfly leaves here (bits of q reversed)
+    const int own = NB == 1 ? 0 : SL == 8 ? (q & 1) << 2 | (q & 2) | q >> 2 : SL == 4 ? (q & 1) << 1 | q >> 1 : q;
+    float4 h[NB];
+    uint2 rb[NB], rc[NB];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        Bv[k] = Elem<T>::get(__ldg(a.bm + b * a.ldb + q * 4 + k));
-        Cv[k] = Elem<T>::get(__ldg(a.cm + b * a.ldc + q * 4 + k));
+    for (int i = 0; i < NB; ++i) {
+        const bool in = b0 + i < a.B;
+        const long long b = in ? b0 + i : 0;
+        h[i] = in && a.h0 != nullptr ? *reinterpret_cast<const float4 *>(a.h0 + (b * a.D + c) * S + q * 4)
+                                     : make_float4(0.f, 0.f, 0.f, 0.f);
+        auto four = [&](const uint16_t *p) -> uint2 {
+            if (BCW) return __ldg(reinterpret_cast<const uint2 *>(p));
+            return make_uint2((uint32_t)__ldg(p) | (uint32_t)__ldg(p + 1) << 16, (uint32_t)__ldg(p + 2) | (uint32_t)__ldg(p + 3) << 16);
+        };
+        rb[i] = four(a.bm + b * a.ldb + q * 4);
+        rc[i] = four(a.cm + b * a.ldc + q * 4);
     }
-    const float zz = a.z != nullptr ? Elem<T>::get(__ldg(a.z + b * a.ldz + c)) : 0.f;
+    const long long bo = b0 + own;
+    const bool mine = bo < a.B;
+    const float u = Elem<T>::get(ld16(a.u + bo * a.ldu + c, mine));
+    const float raw = Elem<T>::get(ld16(a.dt + bo * a.lddt + c, mine)) + (a.dtb != nullptr ? __ldg(a.dtb + c) : 0.f);
+    const float z = Elem<T>::get(ld16(a.z + bo * a.ldz + c, mine && a.z != nullptr));
+    const float4 A = __ldg(reinterpret_cast<const float4 *>(a.A + (long long)c * S + q * 4));
+    const float2 A0 = make_float2(A.x * kLog2e, A.y * kLog2e), A1 = make_float2(A.z * kLog2e, A.w * kLog2e);
+    const float Dk = a.Dk != nullptr ? __ldg(a.Dk + c) : 0.f;
     const float t = a.softplus ? softplus_f(raw) : raw, x = t * u;
-    h.x = fmaf(ex2(t * (A.x * kLog2e)), h.x, x * Bv[0]);
-    h.y = fmaf(ex2(t * (A.y * kLog2e)), h.y, x * Bv[1]);
-    h.z = fmaf(ex2(t * (A.z * kLog2e)), h.z, x * Bv[2]);
-    h.w = fmaf(ex2(t * (A.w * kLog2e)), h.w, x * Bv[3]);
-    if (live && a.hf != nullptr) *reinterpret_cast<float4 *>(a.hf + ch * S + q * 4) = h;
-    float y = fmaf(Cv[0], h.x, fmaf(Cv[1], h.y, fmaf(Cv[2], h.z, Cv[3] * h.w)));
+    float y[NB];
 #pragma unroll
-    for (int o = 1; o < SL; o *= 2) y += __shfl_xor_sync(0xffffffffu, y, o);
-    if (live && q == 0) {
-        if (a.Dk != nullptr) y = fmaf(__ldg(a.Dk + c), u, y);
-        if (a.z != nullptr) y *= zz * sigmoid_f(zz);
-        a.out[ch] = Elem<T>::put(y);
-        if (Elem<T>::bad(y)) set_error(kOpsErrRange);
+    for (int i = 0; i < NB; ++i) {
+        float ti = t, xi = x;
+        if (NB > 1) {   // from the lane that prepared sequence i: the bits of i reversed
+            const int from = (lane & ~(SL - 1)) + (SL == 8 ? (i & 1) << 2 | (i & 2) | i >> 2 : SL == 4 ? (i & 1) << 1 | i >> 1 : i);
+            ti = __shfl_sync(0xffffffffu, t, from);
+            xi = __shfl_sync(0xffffffffu, x, from);
+        }
+        const float2 m0 = __fmul2_rn(splat(ti), A0), m1 = __fmul2_rn(splat(ti), A1);
+        const float2 h0 = __ffma2_rn(make_float2(ex2(m0.x), ex2(m0.y)), make_float2(h[i].x, h[i].y), __fmul2_rn(splat(xi), Elem<T>::get2(rb[i].x)));
+        const float2 h1 = __ffma2_rn(make_float2(ex2(m1.x), ex2(m1.y)), make_float2(h[i].z, h[i].w), __fmul2_rn(splat(xi), Elem<T>::get2(rb[i].y)));
+        if (b0 + i < a.B && a.hf != nullptr)
+            *reinterpret_cast<float4 *>(a.hf + ((b0 + i) * a.D + c) * S + q * 4) = make_float4(h0.x, h0.y, h1.x, h1.y);
+        const float2 y2 = __ffma2_rn(Elem<T>::get2(rc[i].x), h0, __fmul2_rn(Elem<T>::get2(rc[i].y), h1));
+        y[i] = y2.x + y2.y;
+    }
+    butterfly<1, SL, NB>(y, lane);
+    if (mine && (NB > 1 || q == 0)) {
+        float o = fmaf(Dk, u, y[0]);
+        if (a.z != nullptr) o *= z * sigmoid_f(z);
+        a.out[bo * a.D + c] = Elem<T>::put(o);
+        if (Elem<T>::bad(o)) set_error(kOpsErrRange);
     }
 }
 
