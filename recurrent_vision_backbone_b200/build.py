@@ -1,4 +1,5 @@
-"""Build the CUDA library in-tree: recurrent_vision_backbone_b200/libgtr_gla.so.
+"""Build the CUDA library in-tree, recurrent_vision_backbone_b200/libgtr_gla.so, and the
+extension module that hands it torch tensors, recurrent_vision_backbone_b200/_ops.so.
 
 Compiles the csrc/*.cu sources for sm_100a only (nvcc cross-compiles without a GPU):
     python -m recurrent_vision_backbone_b200.build [--verbose]
@@ -9,6 +10,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 import tempfile
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -20,6 +22,9 @@ DEPS = SOURCES + [os.path.join(CSRC, n) for n in ("sm100_ptx.cuh", "gla_fwd_span
 DEPS += [os.path.join(ROOT, "include", n) for n in ("gtr_gla.h", "gtr_swiglu.h", "gtr_gla_bwd.h", "gtr_ops.h", "gtr_ssm.h",
                                                     "gtr_norm.h")]
 LIB = os.path.join(HERE, "libgtr_gla.so")
+BINDING_SOURCE = os.path.join(CSRC, "binding.cpp")
+BINDING_DEPS = [BINDING_SOURCE] + [os.path.join(ROOT, "include", n) for n in ("gtr_gla.h", "gtr_ops.h", "gtr_ssm.h", "gtr_norm.h")]
+BINDING = os.path.join(HERE, "_ops.so")
 
 
 def nvcc_path() -> str:
@@ -39,14 +44,29 @@ def nvcc_cmd(out: str = LIB, extra=(), inputs=None) -> list:
 def compile_cmd(src: str, obj: str, extra=()) -> list:
     """The command that compiles one source (the options of nvcc_cmd)."""
     return [nvcc_path(), "-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo", "-O3",
-            "-std=c++17", "-Xcompiler", "-fPIC", "-I", os.path.join(ROOT, "include"), *extra, "-c", src, "-o", obj]
+            "-std=c++17", "-split-compile=0", "-Xcompiler", "-fPIC", "-I", os.path.join(ROOT, "include"), *extra,
+            "-c", src, "-o", obj]
 
 
-def is_stale(out: str = LIB) -> bool:
+def binding_cmd(out: str) -> list:
+    """The command that compiles the extension module against the installed torch and links it to
+    the CUDA library beside it."""
+    import torch
+    base = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(nvcc_path()))
+    inc = [os.path.join(ROOT, "include"), os.path.join(base, "include"),
+           os.path.join(base, "include", "torch", "csrc", "api", "include"), os.path.join(cuda, "include"),
+           sysconfig.get_paths()["include"]]
+    return ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", *(a for i in inc for a in ("-I", i)), BINDING_SOURCE, "-o", out,
+            "-L", HERE, "-l:libgtr_gla.so", "-L", os.path.join(base, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu",
+            "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN"]
+
+
+def is_stale(out: str = LIB, deps=None) -> bool:
     if not os.path.exists(out):
         return True
     t = os.path.getmtime(out)
-    return any(os.path.getmtime(d) > t for d in DEPS)
+    return any(os.path.getmtime(d) > t for d in (DEPS if deps is None else deps))
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
@@ -61,6 +81,10 @@ def build(force: bool = False, verbose: bool = False) -> str:
                 raise subprocess.CalledProcessError(max(codes, key=abs), "nvcc")
             subprocess.run(nvcc_cmd(tmp, inputs=objs), check=True)
         os.replace(tmp, LIB)
+    if force or is_stale(BINDING, BINDING_DEPS):
+        tmp = BINDING + ".tmp"
+        subprocess.run(binding_cmd(tmp), check=True)
+        os.replace(tmp, BINDING)
     return LIB
 
 

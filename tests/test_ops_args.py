@@ -6,6 +6,7 @@ import ctypes
 import pytest
 
 from recurrent_vision_backbone_b200 import build, gla, norm, ssm
+from tests import ops_abi
 
 MB = 1 << 24   # fake buffers 16 MiB apart
 BAD, UNSUP = gla.GTR_ERR_INVALID_ARG, gla.GTR_ERR_UNSUPPORTED
@@ -21,7 +22,7 @@ def P(x):
 
 
 def conv(x=1, w=2, bias=3, init=4, B=2, H=8, W=8, D=64, K=4, direction=0, dtype=0, act=1, ldx=0):
-    return ssm._Conv(B, H, W, D, K, direction, dtype, act, P(x), ldx, P(w), P(bias), P(init))
+    return ops_abi.Conv(B, H, W, D, K, direction, dtype, act, P(x), ldx, P(w), P(bias), P(init))
 
 
 CONV_BAD = [(dict(B=0), BAD), (dict(D=0), BAD), (dict(H=-1), BAD), (dict(direction=4), BAD), (dict(dtype=2), BAD),
@@ -55,7 +56,7 @@ def test_conv_backward_refusals(lib, bad, code):
 
 def scan(u=1, dt=2, Bm=3, Cm=4, z=5, A=6, D=7, bias=8, init=9, B=2, H=64, W=64, C=64, S=16, direction=0, dtype=0,
          softplus=1, ldu=0, lddt=0, ldb=0, ldc=0, ldz=0):
-    return ssm._Ssm(B, H, W, C, S, direction, dtype, softplus, P(u), P(dt), P(Bm), P(Cm), P(z), ldu, lddt, ldb, ldc, ldz,
+    return ops_abi.Ssm(B, H, W, C, S, direction, dtype, softplus, P(u), P(dt), P(Bm), P(Cm), P(z), ldu, lddt, ldb, ldc, ldz,
                     P(A), P(D), P(bias), P(init))
 
 
@@ -89,7 +90,7 @@ def test_scan_backward_refusals(lib, bad, code):
                 grads=1)
     a = {k: bad.pop(k, v) for k, v in base.items()}
     m = scan(**bad)
-    g = ssm._SsmGrads(P(a["gu"]), P(a["gdt"]), P(a["gB"]), P(a["gC"]), P(a["gz"]), P(a["gA"]), P(a["gD"]), P(a["gt"]), P(a["gi"]))
+    g = ops_abi.SsmGrads(P(a["gu"]), P(a["gdt"]), P(a["gB"]), P(a["gC"]), P(a["gz"]), P(a["gA"]), P(a["gD"]), P(a["gt"]), P(a["gi"]))
     assert lib.gtr_ssm_scan_bwd(ctypes.byref(m), P(a["dy"]), a["ld"], P(a["df"]), ctypes.byref(g) if a["grads"] else None,
                                 P(a["ws"]), a["wsb"], None) == code
 
