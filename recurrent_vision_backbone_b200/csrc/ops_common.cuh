@@ -152,6 +152,12 @@ __device__ __forceinline__ void copy16_async(void *dst, const void *src, uint32_
                  "l"(src), "r"(bytes)
                  : "memory");
 }
+__device__ __forceinline__ void copy4_async(void *dst, const void *src, uint32_t bytes) {   // 4 or 0 of 4 bytes
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(
+                     static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
+                 "l"(src), "r"(bytes)
+                 : "memory");
+}
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>   // waits until at most N of this thread's groups are in flight
 __device__ __forceinline__ void copy_wait() {
@@ -296,19 +302,21 @@ struct Walk {
                 n = (H - 1 - r) * W + x, step = -W, jump = H * W + 1;
         }
     }
+    // (sums modulo 2^32: a step of several rows may pass 31 bits before the jumps bring it back)
+    __device__ __forceinline__ void add(uint32_t d) { n = (int)((uint32_t)n + d); }
     __device__ __forceinline__ void next() {
-        n += step;
+        add((uint32_t)step);
         if (++i == inner) {
             i = 0;
-            n += jump;
+            add((uint32_t)jump);
         }
     }
     __device__ __forceinline__ void advance(int k) {
-        n += k * step;
+        add((uint32_t)k * (uint32_t)step);
         i += k;
         while (i >= inner) {
             i -= inner;
-            n += jump;
+            add((uint32_t)jump);
         }
     }
 };

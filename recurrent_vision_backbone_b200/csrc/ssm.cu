@@ -487,9 +487,9 @@ extern "C" gtr_status_t gtr_ssm_scan_fwd(const gtr_ssm_t *ssm, void *out, float 
     a.tiles = (a.D + sc::kThreads - 1) / sc::kThreads;
     a.hs = static_cast<float *>(workspace);
     a.sdt = a.hs + align256((size_t)a.B * a.P * a.D * state_pad(a.S) * sizeof(float)) / sizeof(float);
-    const void *ps[] = {a.u, a.dt, a.z};
+    const void *ps[] = {a.u, a.dt, a.z, a.out};
     const long long lds[] = {a.ldu, a.lddt, a.z ? a.ldz : 0};
-    const bool wide = rows_on(16, a.D, ps, 3, lds, 3);
+    const bool wide = rows_on(16, a.D, ps, 4, lds, 3);
     return ops_cuda_status(ssm->dtype == GTR_F16 ? scan_fwd_dispatch<__half>(a, p.SL, wide, s)
                                                  : scan_fwd_dispatch<__nv_bfloat16>(a, p.SL, wide, s));
 }

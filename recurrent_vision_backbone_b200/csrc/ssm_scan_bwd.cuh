@@ -18,7 +18,7 @@
 //
 // Layout: a lane holds two neighbouring channels by four states.  The sums over channels (dB, dC:
 // 8 values a token) and over states (q, r, y: 6 values) are butterflies that halve the number
-// of values at every round, so that a token costs 7 + 6 exchanges at 16 states; four states by
+// of values at every round, so that a token costs 7 + 5 exchanges at 16 states; four states by
 // two channels is where the two together are least.  The scalars of a sub-chunk (t, x, e and
 // what the gradients of u, dt, z need) are computed once per channel, spread over the warp.
 #pragma once
@@ -26,7 +26,7 @@
 namespace gtr {
 namespace sc {
 
-constexpr int kSub = 4, kMaxChunkBwd = 56;
+constexpr int kSub = 4, kMaxChunkBwd = 48, kAhead = 2;
 
 template <int SP>
 struct GradLayout {
@@ -48,6 +48,7 @@ __global__ void __launch_bounds__(kThreads, 3) ssm_grad_kernel(const Args a) {
     extern __shared__ __align__(16) float sm[];
     chain_wait();
     __shared__ int stok[kMaxChunkBwd];                           // tokens of the chunk
+    __shared__ uint32_t raw[kAhead + 1][4][NE][kThreads];        // u, dt, d_out, z entries on their way
     const int L = a.L;
     float *sB = sm, *sC = sB + L * SP;
     float4 *ck = reinterpret_cast<float4 *>(sC + L * SP);        // [L / kSub][2][kThreads]
@@ -111,10 +112,11 @@ __global__ void __launch_bounds__(kThreads, 3) ssm_grad_kernel(const Args a) {
     const float2 dtb = param(a.dtb), Dk = param(a.Dk);
     float2 accD = splat(0.f), accT = splat(0.f);
     bool bad = false;
-    uint32_t qu[NE], qt[NE], qy[NE], qz[NE];
-    auto pair_at = [&](const uint16_t *p, long long at, bool in) -> uint32_t {
-        if (PAIRS) return in && e0 ? __ldg(reinterpret_cast<const uint32_t *>(p + at)) : 0u;
-        return (uint32_t)ld16(p + at, in && e0) | (uint32_t)ld16(p + at + 1, in && e1) << 16;
+    auto put_entry = [&](uint32_t *dst, const uint16_t *p, long long at, bool in) {
+        if (PAIRS)
+            copy4_async(dst, p + at, in && e0 ? 4u : 0u);
+        else
+            *dst = (uint32_t)ld16(p + at, in && e0) | (uint32_t)ld16(p + at + 1, in && e1) << 16;
     };
     auto put_pair = [&](uint16_t *p, long long at, float2 v) {
         const uint32_t w = Elem<T>::put2(v.x, v.y);
@@ -127,19 +129,29 @@ __global__ void __launch_bounds__(kThreads, 3) ssm_grad_kernel(const Args a) {
         }
     };
     auto entry = [&](int e) { return (lane + 32 * e) / (CW / 2); };   // token of the sub-chunk
-    auto fetch = [&](int s, bool all) {
+    // The block's steps: the sweep over the sub-chunks but the last, then all from the last back.  A lane's
+    // entries come through shared memory, each lane reading only its own, kAhead steps ahead.
+    const int last_step = 2 * nsub - 2;
+    auto fetch = [&](int k) {
+        const int s = k < nsub - 1 ? k : last_step - k;
+        uint32_t(*dst)[NE][kThreads] = raw[k % (kAhead + 1)];
 #pragma unroll
         for (int e = 0; e < NE; ++e) {
             const int q = s * kSub + entry(e);
-            const bool in = s >= 0 && entry(e) < kSub && q < p1 - p0;
+            const bool in = k <= last_step && entry(e) < kSub && q < p1 - p0;
             const long long row = row0 + (in ? stok[q] : 0);
-            qu[e] = pair_at(a.u, row * a.ldu + ec, in);
-            qt[e] = pair_at(a.dt, row * a.lddt + ec, in);
-            if (all) {
-                qy[e] = pair_at(a.dy, row * a.lddy + ec, in);
-                qz[e] = pair_at(a.z, row * a.ldz + ec, in && gate);
+            put_entry(&dst[0][e][tid], a.u, row * a.ldu + ec, in);
+            put_entry(&dst[1][e][tid], a.dt, row * a.lddt + ec, in);
+            if (k >= nsub - 1) {
+                put_entry(&dst[2][e][tid], a.dy, row * a.lddy + ec, in);
+                if (gate) put_entry(&dst[3][e][tid], a.z, row * a.ldz + ec, in);
             }
         }
+        if (PAIRS) copy_commit();
+    };
+    auto arrived = [&](int k) {   // the entries of step k
+        if (PAIRS) copy_wait<kAhead - 1>();
+        return raw[k % (kAhead + 1)];
     };
     auto put2 = [](float *p, float2 v) { *reinterpret_cast<float2 *>(p) = v; };
     // a token forward: the decays, and the states after it
@@ -162,24 +174,26 @@ __global__ void __launch_bounds__(kThreads, 3) ssm_grad_kernel(const Args a) {
     __syncthreads();
 
     // sweep: checkpoints of the states entering the sub-chunks
-    fetch(0, nsub == 1);
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) fetch(k);
     for (int s = 0; s < nsub; ++s) {
         ck[(s * 2 + 0) * kThreads + tid] = make_float4(h[0][0].x, h[0][0].y, h[0][1].x, h[0][1].y);
         ck[(s * 2 + 1) * kThreads + tid] = make_float4(h[1][0].x, h[1][0].y, h[1][1].x, h[1][1].y);
         if (s == nsub - 1) break;
         __syncwarp();
+        const auto *in = arrived(s);
 #pragma unroll
         for (int e = 0; e < NE; ++e) {   // every sub-chunk but the last is whole
             if (entry(e) >= kSub) break;
             const int ix = entry(e) * CW + el;
-            const float2 raw = __fadd2_rn(Elem<T>::get2(qt[e]), dtb);
-            float2 x, t = softplus_2(raw, x);   // selected, not branched over
-            t = make_float2(sp_on ? t.x : raw.x, sp_on ? t.y : raw.y);
+            const float2 pre = __fadd2_rn(Elem<T>::get2(in[1][e][tid]), dtb);
+            float2 x, t = softplus_2(pre, x);   // selected, not branched over
+            t = make_float2(sp_on ? t.x : pre.x, sp_on ? t.y : pre.y);
             put2(st + ix, t);
-            put2(sx + ix, __fmul2_rn(t, Elem<T>::get2(qu[e])));
+            put2(sx + ix, __fmul2_rn(t, Elem<T>::get2(in[0][e][tid])));
         }
         __syncwarp();
-        fetch(s + 1, s + 1 == nsub - 1);
+        fetch(s + kAhead);
         float2 d[2][2];
 #pragma unroll
         for (int tt = 0; tt < kSub; ++tt) forward(s, tt, d);
@@ -192,18 +206,19 @@ __global__ void __launch_bounds__(kThreads, 3) ssm_grad_kernel(const Args a) {
         const int q0 = s * kSub, m = FULL ? kSub : p1 - p0 - q0;
         float2 eu[NE], et[NE], ee[NE], esg[NE], ez[NE], esz[NE], ey[NE];   // u, t, e, dt / d raw, z, sigmoid(z), d_out
         __syncwarp();
+        const auto *in = arrived(last_step - s);
 #pragma unroll
         for (int e = 0; e < NE; ++e) {
             if (entry(e) >= kSub) break;
             const int ix = entry(e) * CW + el;
-            eu[e] = Elem<T>::get2(qu[e]);
-            ey[e] = Elem<T>::get2(qy[e]);
-            ez[e] = Elem<T>::get2(qz[e]);
-            const float2 raw = __fadd2_rn(Elem<T>::get2(qt[e]), dtb);
+            eu[e] = Elem<T>::get2(in[0][e][tid]);
+            ey[e] = Elem<T>::get2(in[2][e][tid]);
+            ez[e] = Elem<T>::get2(gate ? in[3][e][tid] : 0u);
+            const float2 pre = __fadd2_rn(Elem<T>::get2(in[1][e][tid]), dtb);
             float2 x;
-            const float2 t = softplus_2(raw, x);
-            et[e] = make_float2(sp_on ? t.x : raw.x, sp_on ? t.y : raw.y);
-            esg[e] = make_float2(sp_on ? sigmoid_of(raw.x, x.x) : 1.f, sp_on ? sigmoid_of(raw.y, x.y) : 1.f);
+            const float2 t = softplus_2(pre, x);
+            et[e] = make_float2(sp_on ? t.x : pre.x, sp_on ? t.y : pre.y);
+            esg[e] = make_float2(sp_on ? sigmoid_of(pre.x, x.x) : 1.f, sp_on ? sigmoid_of(pre.y, x.y) : 1.f);
             esz[e] = make_float2(sigmoid_f(ez[e].x), sigmoid_f(ez[e].y));
             const float2 eg = __fmul2_rn(ey[e], __fmul2_rn(ez[e], esz[e]));
             ee[e] = make_float2(gate ? eg.x : ey[e].x, gate ? eg.y : ey[e].y);
@@ -212,7 +227,7 @@ __global__ void __launch_bounds__(kThreads, 3) ssm_grad_kernel(const Args a) {
             put2(se + ix, ee[e]);
         }
         __syncwarp();
-        fetch(s - 1, true);
+        fetch(last_step - s + kAhead);
         float2 d[kSub][2][2], hp[kSub][2][2];   // decays; states entering the tokens
         {
             const float4 c0 = ck[(s * 2 + 0) * kThreads + tid], c1 = ck[(s * 2 + 1) * kThreads + tid];
@@ -239,7 +254,7 @@ __global__ void __launch_bounds__(kThreads, 3) ssm_grad_kernel(const Args a) {
             const float2 Bv[2] = {make_float2(B.x, B.y), make_float2(B.z, B.w)};
             const float2 Cv[2] = {make_float2(C.x, C.y), make_float2(C.z, C.w)};
             float2 vb[2], vc[2];                           // dB, dC of this lane's channels
-            float vs[8];                                   // q, r, y of both channels, two unused
+            float vs[4], vr[2];                            // q and y of both channels; r of both
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 const float2 tk = splat(k ? t.y : t.x), xk = splat(k ? x.y : x.x), ek = splat(k ? e.y : e.x);
@@ -258,9 +273,8 @@ __global__ void __launch_bounds__(kThreads, 3) ssm_grad_kernel(const Args a) {
                     g[k][i] = Ga;
                 }
                 vs[k] = q.x + q.y;
-                vs[2 + k] = r.x + r.y;
-                vs[4 + k] = y.x + y.y;
-                vs[6 + k] = 0.f;
+                vs[2 + k] = y.x + y.y;
+                vr[k] = r.x + r.y;
             }
             float vbc[8] = {vb[0].x, vb[0].y, vb[1].x, vb[1].y, vc[0].x, vc[0].y, vc[1].x, vc[1].y};
             const int ib = butterfly<SL, 32, 8>(vbc, lane);   // over the channels of the warp
@@ -270,13 +284,14 @@ __global__ void __launch_bounds__(kThreads, 3) ssm_grad_kernel(const Args a) {
                 const int v = ib + i;   // 0..3 dB, 4..7 dC of states sl * 4 + v % 4
                 ws[tt * 2 * SP + (v >= 4 ? SP : 0) + sl * 4 + (v & 3)] = vbc[i];
             }
-            const int is = butterfly<1, SL, 8>(vs, lane);     // over the states of the channels
-            constexpr int ls = left_of(8, SL);
+            // over the states of the channels: q and y halve from four values, r from two
+            const int is = butterfly<1, SL, 4>(vs, lane), ir = butterfly<1, SL, 2>(vr, lane);
+            constexpr int ls = left_of(4, SL), lr = left_of(2, SL);
 #pragma unroll
-            for (int i = 0; i < ls; ++i) {
-                const int v = is + i;   // q, q, r, r, y, y, -, -
-                if (v < 6) rq[(v >> 1) * kSub * CW + tt * CW + 2 * pr + (v & 1)] = vs[i];
-            }
+            for (int i = 0; i < ls; ++i)   // q, q, y, y
+                (is + i >= 2 ? ry : rq)[tt * CW + 2 * pr + ((is + i) & 1)] = vs[i];
+#pragma unroll
+            for (int i = 0; i < lr; ++i) rr[tt * CW + 2 * pr + ir + i] = vr[i];
         }
         __syncthreads();   // the warps' sums of dB, dC (two buffers: the next sub-chunk writes the other)
         for (int i = tid; i < m * 2 * SP; i += kThreads) {

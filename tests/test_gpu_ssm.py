@@ -447,6 +447,63 @@ def test_another_stream_than_the_current_one():
     assert torch.equal(got, want) and all(torch.equal(a, b) for a, b in zip(gg, gw))
 
 
+def off_grid(t):
+    """The same values two bytes further on than the allocator's boundaries."""
+    return torch.cat((t.new_zeros(1), t.reshape(-1)))[1:].view(t.shape)
+
+
+@pytest.mark.parametrize("N", [1, 90, 700])
+def test_each_tensor_off_the_16_byte_grid(N):
+    """Rows of whole 16-byte pieces whose tensors start two bytes off, one tensor at a time: the
+    results are those of aligned tensors, bit for bit."""
+    dev, D = torch.device("cuda", 0), 128
+    _, d = scan_inputs(2, 1, N, D, 16, torch.float16, dev, seed=N)
+    want, wf = run_scan(d, 1, N, 0, init_state=d["init"], final_state=True)
+    wg = run_scan_bwd(d, 1, N, 0)
+    for name in ("u", "dt", "Bm", "Cm", "z", "dy", "out"):
+        o = dict(d, **{name: off_grid(d[name])}) if name != "out" else d
+        out = off_grid(torch.empty_like(want)) if name == "out" else None
+        got, gf = run_scan(o, 1, N, 0, init_state=d["init"], final_state=True, out=out)
+        assert torch.equal(got, want) and torch.equal(gf, wf), name
+        grads = tuple(off_grid(torch.empty_like(g)) if name == "out" and g.dtype == torch.float16 else torch.empty_like(g)
+                      for g in wg)
+        for a, b in zip(run_scan_bwd(o, 1, N, 0, grads=grads), wg):
+            assert torch.equal(a, b), name
+    _, e = conv_inputs(2, 1, N, D, 4, torch.float16, True, True, dev, seed=N)
+    conv = lambda e, **kw: ssm.gtr_causal_conv_fwd(e["x"], e["w"], 1, N, 0, bias=e["b"], init_state=e["init"], **kw)  # noqa: E731
+    back = lambda e, **kw: ssm.gtr_causal_conv_bwd(e["x"], e["w"], e["dy"], 1, N, 0, bias=e["b"], init_state=e["init"],  # noqa: E731
+                                                   d_final_state=e["df"], **kw)
+    want, wf = conv(e, final_state=True)
+    wg = back(e)
+    for name in ("x", "init", "dy", "df", "out", "fin"):
+        o = dict(e, **{name: off_grid(e[name])}) if name in e else e
+        got, gf = conv(o, out=off_grid(torch.empty_like(want)) if name == "out" else None,
+                       final_state=off_grid(torch.empty_like(wf)) if name == "fin" else True)
+        assert torch.equal(got, want) and torch.equal(gf, wf), name
+        grads = tuple(off_grid(torch.empty_like(g)) if name == "out" and g.dtype == torch.float16 else torch.empty_like(g)
+                      for g in wg)
+        for a, b in zip(back(o, grads=grads), wg):
+            assert torch.equal(a, b), name
+    assert gla.device_status() == gla.GTR_OK
+
+
+def test_calls_at_the_same_time_on_two_streams():
+    dev = torch.device("cuda", 0)
+    ds = [scan_inputs(1, 20, 50, 96, 16, torch.bfloat16, dev, seed=s)[1] for s in (1, 2)]
+    want = [(run_scan(d, 20, 50, 2), run_scan_bwd(d, 20, 50, 2)) for d in ds]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = []
+    for _ in range(5):
+        for d, s in zip(ds, streams):
+            with torch.cuda.stream(s):
+                got.append((run_scan(d, 20, 50, 2), run_scan_bwd(d, 20, 50, 2)))
+    torch.cuda.synchronize()
+    for i, (f, g) in enumerate(got):
+        wf, wg = want[i % 2]
+        assert torch.equal(f[0], wf[0]) and all(torch.equal(a, b) for a, b in zip(g, wg))
+
+
 def test_channels_past_32_bit_offsets():
     """Rows more than 2^31 elements into a tensor (a slice of very wide rows)."""
     dev, N, D = torch.device("cuda", 0), 40, 64

@@ -149,3 +149,14 @@ def test_bindings_refuse_host_tensors(lib):
         norm.gtr_group_norm_fwd(x, 4)
     with pytest.raises(ValueError):
         norm.gtr_group_norm_bwd(x, x, f(1, 4, 2), 4)
+
+
+def test_headers_compile_as_c(tmp_path):
+    import os
+    import subprocess
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    src = tmp_path / "t.c"
+    src.write_text('#include "gtr_ssm.h"\n#include "gtr_norm.h"\n'
+                   "int main(void){ gtr_conv_t c; gtr_ssm_t m; return (int)(sizeof(c) + sizeof(m)) * 0 + (int)GTR_F16; }\n")
+    subprocess.run(["gcc", "-std=c99", "-Wall", "-Werror", "-I", os.path.join(root, "include"), str(src), "-o",
+                    str(tmp_path / "t")], check=True)
