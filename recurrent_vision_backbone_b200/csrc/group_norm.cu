@@ -133,7 +133,7 @@ __device__ __forceinline__ float2 slope(float2 dy, float2 z) {
 
 template <typename T, bool BWD, bool SILU>
 __global__ void __launch_bounds__(32 * kLanes, 3) group_norm_figures_kernel(const Args a) {
-    constexpr int AT = BWD ? 4 : 8;   // rows asked for at once
+    constexpr int AT = BWD ? 2 : 4;   // rows of a batch; the next batch is asked for before one is used
     __shared__ float red[kLanes][32][BWD ? 17 : 3];
     __shared__ float2 chan[32 * 8];
     chain_wait();
@@ -158,14 +158,24 @@ __global__ void __launch_bounds__(32 * kLanes, 3) group_norm_figures_kernel(cons
             params4(a.beta, c, 0.f, bet);
         }
     }
+    Raw<8> rx[AT], rd[AT], nx[AT], nd[AT];
+    auto fetch = [&](int r) {
+#pragma unroll
+        for (int u = 0; u < AT; ++u) {
+            const bool in = live && r + u * kLanes < r1;
+            nx[u] = in ? load_raw<8>(a.x + base + (long long)(r + u * kLanes) * a.C) : zero_raw<8>();
+            if (BWD) nd[u] = in ? load_raw<8>(a.dy + base + (long long)(r + u * kLanes) * a.C) : zero_raw<8>();
+        }
+    };
+    fetch(r0 + y);
     for (int r = r0 + y; live && r < r1; r += kLanes * AT) {
-        Raw<8> rx[AT], rd[AT];
         const int k = min((r1 - r + kLanes - 1) / kLanes, AT);
 #pragma unroll
         for (int u = 0; u < AT; ++u) {
-            rx[u] = u < k ? load_raw<8>(a.x + base + (long long)(r + u * kLanes) * a.C) : zero_raw<8>();
-            if (BWD) rd[u] = u < k ? load_raw<8>(a.dy + base + (long long)(r + u * kLanes) * a.C) : zero_raw<8>();
+            rx[u] = nx[u];
+            if (BWD) rd[u] = nd[u];
         }
+        fetch(r + kLanes * AT);
         if (BWD) {
 #pragma unroll
             for (int u = 0; u < AT; ++u) {
@@ -261,7 +271,7 @@ __global__ void __launch_bounds__(32 * kLanes, 3) group_norm_figures_kernel(cons
 // block, over batch entries and token ranges in a fixed order.
 template <typename T, bool BWD, bool SILU>
 __global__ void __launch_bounds__(32 * kLanes, 3) group_norm_results_kernel(const Args a, int blocks) {
-    constexpr int AT = BWD ? 2 : 4;   // rows asked for at once
+    constexpr int AT = 2;   // rows of a batch; the next batch is asked for before one is used
     __shared__ float2 fig[32];
     __shared__ float2 cols[kLanes][33];
     chain_wait();
@@ -290,13 +300,13 @@ __global__ void __launch_bounds__(32 * kLanes, 3) group_norm_results_kernel(cons
     const int r0 = s * a.rows, r1 = min(a.N, r0 + a.rows);
     const bool live = x < pc.n;
     const long long base = (long long)b * a.N * a.C + c;
-    Raw<8> rx[AT], rd[AT];
+    Raw<8> rx[AT], rd[AT], nx[AT], nd[AT];
     auto fetch = [&](int r) {
 #pragma unroll
         for (int u = 0; u < AT; ++u) {
             const bool in = live && r + u * kLanes < r1;
-            rx[u] = in ? load_raw<8>(a.x + base + (long long)(r + u * kLanes) * a.C) : zero_raw<8>();
-            if (BWD) rd[u] = in ? load_raw<8>(a.dy + base + (long long)(r + u * kLanes) * a.C) : zero_raw<8>();
+            nx[u] = in ? load_raw<8>(a.x + base + (long long)(r + u * kLanes) * a.C) : zero_raw<8>();
+            if (BWD) nd[u] = in ? load_raw<8>(a.dy + base + (long long)(r + u * kLanes) * a.C) : zero_raw<8>();
         }
     };
     fetch(r0 + y);
@@ -322,6 +332,12 @@ __global__ void __launch_bounds__(32 * kLanes, 3) group_norm_results_kernel(cons
     }
     uint32_t worst = 0;
     for (int r = r0 + y; r < r1; r += kLanes * AT) {
+#pragma unroll
+        for (int u = 0; u < AT; ++u) {
+            rx[u] = nx[u];
+            if (BWD) rd[u] = nd[u];
+        }
+        fetch(r + kLanes * AT);
         Raw<8> o[AT];
 #pragma unroll
         for (int u = 0; u < AT; ++u) {
@@ -343,7 +359,6 @@ __global__ void __launch_bounds__(32 * kLanes, 3) group_norm_results_kernel(cons
                 o[u].w[v] = Elem<T>::put2(q.x, q.y);
             }
         }
-        fetch(r + kLanes * AT);
 #pragma unroll
         for (int u = 0; u < AT; ++u)
             if (r + u * kLanes < r1) {
