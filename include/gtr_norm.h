@@ -9,17 +9,17 @@
  *
  * Layouts (device pointers):
  *     x, out, d_out, grad_x   16-bit elements of one type (gtr_dtype_t), [B, N, C] dense,
- *                             aligned to 2 bytes (16 where C / groups is a multiple of 8:
- *                             the faster kernels)
+ *                             aligned to 2 bytes (tensors on 16 bytes with C / groups a
+ *                             multiple of 8 take the faster kernels)
  *     gamma, beta             float32 [C], each may be NULL (1 and 0)
  *     stats                   float32 [B, groups, 2]: mean, rstd
  * float32 tensors and the workspace are 16-byte aligned.
  *
  * Ownership, streams and errors as in gtr_gla.h: every buffer is the caller's, all work is
  * enqueued on `stream`, nothing synchronises the host and no call keeps anything.  out may be x
- * itself; nothing else may overlap.  Statistics and sums are held in float32, the variance as a
- * sum of squared deviations from a mean (never as a difference of squares), and sums are taken in
- * a fixed order: equal calls give equal bits.  An fp16 output that left the fp16 range (or is
+ * itself; nothing else may overlap.  Statistics and sums are held in float32, the variance as
+ * parts of (count, mean, squared deviations) that are merged (so a mean far above the spread costs
+ * no accuracy), and sums are taken in a fixed order: equal calls give equal bits.  An fp16 output that left the fp16 range (or is
  * NaN) sets GTR_ERR_RANGE in the device error word (gtr_gla_device_status).
  *   GTR_ERR_INVALID_ARG   null, misaligned, overlapping or negative arguments, groups that do
  *                         not divide C, an eps that is negative or not finite, an unknown type

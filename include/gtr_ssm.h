@@ -25,7 +25,7 @@
  *     scan init_state, final_state and their gradients: float32 [B, D, S] dense
  *     w float32 [D][K]; bias, D, dt_bias float32 [D]; A float32 [D][S]; grad_ of these alike
  * Activations are aligned to their 2 bytes, float32 tensors and the workspace to 16; sizes
- * and strides are otherwise free (whole 16-byte rows take wider loads in the convolution).
+ * and strides are otherwise free (rows of whole 16-byte pieces on 16 bytes are copied faster).
  *
  * Ownership, streams and errors as in gtr_gla.h: every buffer is the caller's, all work is
  * enqueued on `stream`, nothing synchronises the host, and no call keeps anything: calls

@@ -16,9 +16,10 @@ import tempfile
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
-SOURCES = [os.path.join(CSRC, n) for n in ("gtr_gla.cu", "ssm.cu", "group_norm.cu")]
+SOURCES = [os.path.join(CSRC, n) for n in ("gtr_gla.cu", "causal_conv.cu", "ssm_scan.cu", "ssm_scan_bwd.cu", "group_norm.cu")]
 DEPS = SOURCES + [os.path.join(CSRC, n) for n in ("sm100_ptx.cuh", "gla_fwd_span.cuh", "gla_fwd_pipe.cuh", "swiglu_gate.cuh", "gla_bwd.cuh",
-                                                  "ops_common.cuh", "causal_conv.cuh", "ssm_scan.cuh", "ssm_scan_bwd.cuh")]
+                                                  "ops_common.cuh", "ops_errors.h", "causal_conv.cuh", "ssm_scan.cuh", "ssm_scan_bwd.cuh",
+                                                  "ssm_host.cuh")]
 DEPS += [os.path.join(ROOT, "include", n) for n in ("gtr_gla.h", "gtr_swiglu.h", "gtr_gla_bwd.h", "gtr_ops.h", "gtr_ssm.h",
                                                     "gtr_norm.h")]
 LIB = os.path.join(HERE, "libgtr_gla.so")
@@ -44,7 +45,7 @@ def nvcc_cmd(out: str = LIB, extra=(), inputs=None) -> list:
 def compile_cmd(src: str, obj: str, extra=()) -> list:
     """The command that compiles one source (the options of nvcc_cmd)."""
     return [nvcc_path(), "-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo", "-O3",
-            "-std=c++17", "-split-compile=0", "-Xcompiler", "-fPIC", "-I", os.path.join(ROOT, "include"), *extra,
+            "-std=c++17", "-Xcompiler", "-fPIC", "-I", os.path.join(ROOT, "include"), *extra,
             "-c", src, "-o", obj]
 
 

@@ -1,5 +1,5 @@
 // causal_conv.cuh -- the short causal convolution over the scan order, forward and backward
-// (included by ssm.cu, which holds the C entry points).
+// (included by causal_conv.cu, which holds the C entry points).
 //
 // Over scan positions p of one sequence, with X = [K - 1 earlier inputs ; x],
 //     s_p = bias + sum_{j<K} w[j] X[p + j],   out_p = act(s_p)

@@ -11,9 +11,6 @@
 #include "ops_common.cuh"
 
 namespace gtr {
-static __device__ unsigned int g_norm_error_word;
-static __device__ __forceinline__ void set_error(unsigned e) { atomicOr(&g_norm_error_word, e); }
-
 namespace gn {
 
 using namespace ops;
@@ -597,15 +594,7 @@ __global__ void __launch_bounds__(32 * kRowLanes) group_norm_apply_kernel(const 
 
 }  // namespace gn
 
-unsigned norm_take_errors() {
-    unsigned word = 0;
-    if (cudaMemcpyFromSymbol(&word, g_norm_error_word, sizeof(word)) != cudaSuccess) return kOpsErrCuda;
-    if (word != 0) {
-        const unsigned zero = 0;
-        if (cudaMemcpyToSymbol(g_norm_error_word, &zero, sizeof(zero)) != cudaSuccess) return kOpsErrCuda;
-    }
-    return word;
-}
+unsigned norm_take_errors() { return take_errors(); }
 
 // ------------------------------------------------------------------ host
 using namespace ops;
@@ -708,7 +697,6 @@ static cudaError_t norm_dispatch(const gn::Args &a, int dtype, cudaStream_t s) {
     if (dtype == GTR_F16) return wide ? norm_launch<__half, 8, BWD>(a, s) : norm_launch<__half, 1, BWD>(a, s);
     return wide ? norm_launch<__nv_bfloat16, 8, BWD>(a, s) : norm_launch<__nv_bfloat16, 1, BWD>(a, s);
 }
-static bool bad_f32(const void *p, bool required) { return p == nullptr ? required : !aligned_to(p, 16); }
 
 }  // namespace gtr
 

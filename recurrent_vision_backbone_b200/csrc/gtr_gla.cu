@@ -163,7 +163,7 @@ namespace gtr {
 // the backward pass: its kernels, then (below) its C entry points
 #include "../../include/gtr_gla_bwd.h"
 #include "gla_bwd.cuh"
-#include "ops_common.cuh"
+#include "ops_errors.h"
 
 namespace gtr {
 enum KernelKind { kSpan = 0, kSpanShort = 1, kSpanZ = 2, kSpanShortZ = 3, kPipe = 4, kPipeZ = 5, kKinds = 6 };
@@ -714,7 +714,7 @@ static gtr_status_t cuda_status(cudaError_t e) {
     cudaGetLastError();   // clear a non-sticky error
     return GTR_ERR_CUDA;
 }
-// the operators of ssm.cu and group_norm.cu report through the same error record
+// the operators beside the token mixer report through the same error record
 gtr_status_t gtr::ops_cuda_status(cudaError_t e) { return cuda_status(e); }
 
 extern "C" gtr_status_t gtr_gla_fwd(const gtr_half_t *q, const gtr_half_t *k,
@@ -1007,7 +1007,7 @@ extern "C" gtr_status_t gtr_gla_device_status(void *stream) {
     }
     unsigned word = 0;
     if (cudaMemcpyFromSymbol(&word, g_error_word, sizeof(word)) != cudaSuccess) return GTR_ERR_CUDA;
-    const unsigned ops_word = ssm_take_errors() | norm_take_errors();   // read and cleared
+    const unsigned ops_word = conv_take_errors() | ssm_take_errors() | ssm_bwd_take_errors() | norm_take_errors();   // read and cleared
     if (ops_word & kOpsErrCuda) return GTR_ERR_CUDA;
     word |= ops_word;
     if (word == kErrRange) {

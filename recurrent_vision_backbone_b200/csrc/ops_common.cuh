@@ -1,4 +1,5 @@
-// ops_common.cuh -- what the operators around the token mixer share (ssm.cu, group_norm.cu):
+// ops_common.cuh -- what the operators around the token mixer share (causal_conv.cu, ssm_scan.cu,
+// ssm_scan_bwd.cu, group_norm.cu):
 // 16-bit element access, scan walks, activations, and the host side of argument checks.
 #pragma once
 
@@ -10,16 +11,22 @@
 #include <cstdint>
 
 #include "../../include/gtr_ops.h"
+#include "ops_errors.h"
 
 namespace gtr {
 
-// Defined in gtr_gla.cu: keeps the error for gtr_gla_last_error and turns it into a status.
-gtr_status_t ops_cuda_status(cudaError_t e);
-// Error bits of one source file's kernels on the current device, read and cleared
-// (gtr_gla_device_status collects them). kOpsErrCuda: the word could not be read.
-constexpr unsigned kOpsErrRange = 2u, kOpsErrCuda = 0x80000000u;
-unsigned ssm_take_errors();
-unsigned norm_take_errors();
+// The error word of this source file's kernels.
+static __device__ unsigned int g_ops_error_word;
+static __device__ __forceinline__ void set_error(unsigned e) { atomicOr(&g_ops_error_word, e); }
+static inline unsigned take_errors() {
+    unsigned word = 0;
+    if (cudaMemcpyFromSymbol(&word, g_ops_error_word, sizeof(word)) != cudaSuccess) return kOpsErrCuda;
+    if (word != 0) {
+        const unsigned zero = 0;
+        if (cudaMemcpyToSymbol(g_ops_error_word, &zero, sizeof(zero)) != cudaSuccess) return kOpsErrCuda;
+    }
+    return word;
+}
 
 namespace ops {
 
@@ -356,7 +363,47 @@ inline bool overlap(const Span &a, const Span &b) {
 inline long long row_bytes(long long rows, long long ld, long long cols) {
     return rows <= 0 ? 0 : ((rows - 1) * ld + cols) * 2;
 }
-constexpr long long kMaxTokens = (1LL << 30) - 1, kMaxElements = 1LL << 40;
+constexpr long long kMaxTokens = (1LL << 30) - 1, kMaxElements = 1LL << 40, kMaxGrid = 0x7fffffffLL;
+
+inline bool bad_common(int B, int H, int W, int D, int dir, int dtype) {
+    if (B <= 0 || D <= 0 || H < 0 || W < 0 || dir < 0 || dir > 3) return true;
+    if (dtype != GTR_F16 && dtype != GTR_BF16) return true;
+    const long long N = (long long)H * W;
+    return N > kMaxTokens || (long long)B * N > kMaxElements / D;
+}
+// A [B, N, cols] activation with rows ld apart: present, aligned, rows that do not overlap.
+inline bool bad_rows(const void *p, long long ld, int cols, long long rows) {
+    if (rows == 0) return ld < 0;
+    return p == nullptr || !aligned_to(p, 2) || (ld != 0 && ld < cols) || (ld > 0 && rows > (kMaxElements << 4) / ld);
+}
+inline bool bad_f32(const void *p, bool required) { return p == nullptr ? required : !aligned_to(p, 16); }
+
+inline bool any_overlap(const Span *outs, int no, const Span *ins, int ni) {
+    for (int i = 0; i < no; ++i) {
+        for (int k = 0; k < ni; ++k)
+            if (overlap(outs[i], ins[k])) return true;
+        for (int k = i + 1; k < no; ++k)
+            if (overlap(outs[i], outs[k])) return true;
+    }
+    return false;
+}
+
+// Whether every row of every tensor starts on a `bytes` boundary and holds whole pieces of them.
+inline bool rows_on(int bytes, int D, const void *const *ps, int np, const long long *lds, int nl) {
+    if (D * 2LL % bytes) return false;
+    for (int i = 0; i < np; ++i)
+        if (ps[i] && !aligned_to(ps[i], bytes)) return false;
+    for (int i = 0; i < nl; ++i)
+        if (lds[i] * 2 % bytes) return false;
+    return true;
+}
+
+// dst = src, or zeros without src.
+inline gtr_status_t copy_or_zero(void *dst, const void *src, size_t bytes, cudaStream_t s) {
+    if (dst == nullptr || dst == src || bytes == 0) return GTR_OK;
+    return ops_cuda_status(src != nullptr ? cudaMemcpyAsync(dst, src, bytes, cudaMemcpyDeviceToDevice, s)
+                                          : cudaMemsetAsync(dst, 0, bytes, s));
+}
 
 }  // namespace ops
 }  // namespace gtr

@@ -1,5 +1,5 @@
 // ssm_scan.cuh -- the selective scan, forward, backward and for single tokens
-// (included by ssm.cu, which holds the C entry points).
+// (included by ssm_scan.cu, which holds the C entry points).
 //
 // Per batch, channel d and state n over scan positions p (t_p the time step, x_p = t_p u_p):
 //     h_p = a_p h_{p-1} + x_p B_p[n],  a_p = exp(t_p A[d][n]),   y_p[d] = sum_n C_p[n] h_p + D u_p

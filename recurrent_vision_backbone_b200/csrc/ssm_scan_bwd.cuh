@@ -1,4 +1,4 @@
-// ssm_scan_bwd.cuh -- gradients of the selective scan (included by ssm.cu after ssm_scan.cuh).
+// ssm_scan_bwd.cuh -- gradients of the selective scan (included by ssm_scan_bwd.cu after ssm_scan.cuh).
 //
 // With h_p = a_p h_{p-1} + x_p B_p, x = t u, e_p = d_out_p silu(z_p) and G_p = dL/dh_p:
 //     G_p = C_p e_p + a_{p+1} G_{p+1}   (+ d_final at the last position)
@@ -368,6 +368,7 @@ __global__ void __launch_bounds__(256) ssm_grad_sum_kernel(const Args a, int bc_
         const int v = (int)(id % (2 * SP)), n = v % SP;
         if (row >= rows || n >= a.S) return;
         float s = 0.f;
+#pragma unroll 8
         for (int k = 0; k < a.tiles; ++k) s += a.pbc[((long long)k * rows + row) * 2 * SP + v];
         (v < SP ? a.dB : a.dC)[row * a.S + n] = Elem<T>::put(s);
         if (Elem<T>::bad(s)) set_error(kOpsErrRange);
@@ -381,6 +382,7 @@ __global__ void __launch_bounds__(256) ssm_grad_sum_kernel(const Args a, int bc_
     if (col < cols) {
         const float *src = col < na ? a.hs + col : col < na + a.D ? a.pd + (col - na) : a.pt + (col - na - a.D);
         const long long stride = col < na ? na : a.D;
+#pragma unroll 8
         for (int r = lane; r < rows; r += 8) s += src[r * stride];
     }
     red[lane][threadIdx.x % 32] = s;
