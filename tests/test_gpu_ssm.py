@@ -75,6 +75,9 @@ CONV = [
     (2, 37, 53, 70, 2, 3, "bf16", False, True, True),   # even channels, no whole 16 bytes
     (1, 1, 1000, 1, 3, 0, "bf16", True, False, False),  # one channel
     (1, 3, 67, 136, 2, 0, "fp16", True, True, True),
+    (2, 64, 64, 520, 4, 1, "fp16", True, True, True),   # blocks enough for eight positions a thread
+    (2, 64, 64, 67, 3, 2, "bf16", True, True, False),   # the same by single elements
+    (40, 5, 9, 384, 4, 3, "bf16", True, True, True),    # many short sequences
 ]
 
 
@@ -182,6 +185,21 @@ SCAN = [
     (2, 6, 50, 96, 16, 1, "fp16", True, True, True, True, True, 40.0),    # decays down to nothing
     (1, 17, 19, 31, 7, 0, "bf16", True, True, False, False, True, 0.02),  # of either sign, within float32
 ]
+SCAN += [
+    # channels enough for one walk over whole sequences, two lanes a channel, then one
+    (100, 2, 9, 40, 16, 1, "fp16", True, True, True, True, True, 1.0),
+    (49, 3, 11, 136, 8, 2, "bf16", True, True, True, True, True, 1.0),
+    (97, 1, 20, 33, 32, 0, "fp16", False, True, True, True, True, 1.0),
+    (450, 1, 5, 24, 16, 3, "bf16", True, True, True, True, True, 1.0),
+    (446, 1, 17, 9, 5, 0, "fp16", True, False, True, True, False, 1.0),
+    # chunks enough for the backward's longer ones
+    (100, 10, 10, 200, 16, 2, "fp16", True, True, True, True, True, 1.0),
+    # many single tokens: as many sequences a thread as lanes share a channel
+    (301, 1, 1, 1027, 4, 0, "fp16", True, True, True, True, True, 1.0),
+    (301, 1, 1, 1027, 8, 0, "bf16", True, True, True, True, True, 1.0),
+    (301, 1, 1, 1027, 16, 0, "fp16", False, True, True, True, False, 1.0),
+    (301, 1, 1, 1027, 32, 0, "fp16", True, True, True, True, True, 1.0),
+]
 # A state that grows past float32 has no float32 value, and neither has what follows from it (an
 # infinity times a decay, or less another, is no number): from the first position of a channel
 # whose terms pass this size there is nothing to compare with.  (The first case of either sign
@@ -278,11 +296,25 @@ def test_scan_long_sequence_with_few_channels():
     check(fin, h.cpu(), mh.cpu(), k, "final state")
 
 
-@pytest.mark.parametrize("N", [1, 7, 200])
-def test_scan_state_carried_in_place(N):
+def test_scan_backward_of_a_long_sequence():
+    """5000 tokens in 157 chunks: the folds run over several batches of them."""
+    dev, N = torch.device("cuda", 0), 5000
+    c, d = scan_inputs(1, 50, 100, 12, 16, torch.bfloat16, dev, seed=19, decay=0.05)
+    got = run_scan_bwd(d, 50, 100, 1)
+    assert gla.device_status() == gla.GTR_OK
+    args = (d["u"], d["dt"], d["A"], d["Bm"], d["Cm"], d["dy"], ref.scan_order(50, 100, 1, dev), d["D"], d["z"],
+            d["dt_bias"], True, d["init"], d["df"])
+    want, mag = ref.scan_bwd(*args), ref.scan_bwd(*args, mag=True)
+    k = 2 * (8 + 8 * exponent(c)) * (N + 8) + N + 28
+    for name, g, w_, m in zip(("u", "dt", "A", "Bm", "Cm", "D", "z", "dt_bias", "init"), got, want, mag):
+        check(g, w_.cpu(), m.cpu(), k, name)
+
+
+@pytest.mark.parametrize("B,N", [(2, 1), (2, 7), (2, 200), (110, 30), (460, 9), (310, 1)])
+def test_scan_state_carried_in_place(B, N):
     """final_state = init_state gives what two tensors give, bit for bit."""
     dev = torch.device("cuda", 0)
-    _, d = scan_inputs(2, 1, N, 96, 16, torch.bfloat16, dev, seed=N)
+    _, d = scan_inputs(B, 1, N, 96 if B < 300 else 1000 if N == 1 else 40, 16, torch.bfloat16, dev, seed=N)
     out, fin = run_scan(d, 1, N, 0, init_state=d["init"], final_state=True)
     st = d["init"].clone()
     out2, _ = run_scan(d, 1, N, 0, init_state=st, final_state=st)
