@@ -80,8 +80,7 @@ struct Elem<__nv_bfloat16> {
     static __device__ __forceinline__ uint32_t worst(uint32_t, uint32_t) { return 0; }
 };
 
-// V consecutive elements as raw words: V = 8 is one 16-byte access, 4 an 8-byte one, 2 a
-// 4-byte one, 1 two bytes.
+// V consecutive elements as raw words: V = 8 is one 16-byte access, V = 1 two bytes.
 template <int V>
 struct Raw {
     uint32_t w[V >= 2 ? V / 2 : 1];
@@ -92,19 +91,13 @@ __device__ __forceinline__ Raw<V> load_raw(const uint16_t *p) {
     if constexpr (V == 8) {
         const uint4 x = __ldg(reinterpret_cast<const uint4 *>(p));
         r.w[0] = x.x, r.w[1] = x.y, r.w[2] = x.z, r.w[3] = x.w;
-    } else if constexpr (V == 4) {
-        const uint2 x = __ldg(reinterpret_cast<const uint2 *>(p));
-        r.w[0] = x.x, r.w[1] = x.y;
-    } else if constexpr (V == 2) {
-        r.w[0] = __ldg(reinterpret_cast<const uint32_t *>(p));
     } else {
+        static_assert(V == 1, "16 or 2 bytes");
         r.w[0] = __ldg(p);
     }
     return r;
 }
-template <int V>
-__device__ __forceinline__ Raw<V> load_raw_shared(const uint16_t *p) {
-    static_assert(V == 8, "16-byte pieces");
+__device__ __forceinline__ Raw<8> load_raw_shared(const uint16_t *p) {
     const uint4 x = *reinterpret_cast<const uint4 *>(p);
     return {{x.x, x.y, x.z, x.w}};
 }
@@ -112,10 +105,6 @@ template <int V>
 __device__ __forceinline__ void store_raw(uint16_t *p, const Raw<V> &r) {
     if constexpr (V == 8)
         *reinterpret_cast<uint4 *>(p) = make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]);
-    else if constexpr (V == 4)
-        *reinterpret_cast<uint2 *>(p) = make_uint2(r.w[0], r.w[1]);
-    else if constexpr (V == 2)
-        *reinterpret_cast<uint32_t *>(p) = r.w[0];
     else
         *p = (uint16_t)r.w[0];
 }

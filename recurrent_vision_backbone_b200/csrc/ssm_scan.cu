@@ -17,9 +17,10 @@ struct ScanPlan {
 };
 // The walks of a forward scan.  With 96 blocks of 128 channels or more, one walk over whole
 // sequences: two lanes a channel until the channels alone are three warps a scheduler, then one (8 x 2304
-// tokens of 2048 channels, 128 blocks: 306 us with two lanes, 425 with one, 384 with four; 397 in four
-// chunks).  Below that, as many chunks as make one wave of four blocks an SM, at least 32 tokens each
-// (16384 tokens of 1024 channels, 8 blocks: 182 us with 74 chunks, 201 with 92, 250 with 37).
+// tokens of 2048 channels, 128 blocks, at one state of the kernels: 348 us with two lanes, 425 with one, 384
+// with four, 425 in four chunks).  Below that, as many chunks as make one wave of four blocks an SM, at
+// least 32 tokens each (16384 tokens of 1024 channels, 8 blocks: 193 us with 74 chunks, 201 with 92, 250
+// with 37).
 static ScanPlan scan_fwd_plan(int B, long long N, int D) {
     const long long base = (long long)B * ((D + sc::kThreads - 1) / sc::kThreads);
     const long long P = base >= 96 ? 1 : kSmAim / base;

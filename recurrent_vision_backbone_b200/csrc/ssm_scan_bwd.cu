@@ -47,7 +47,9 @@ static cudaError_t scan_bwd_launch(sc::Args a, bool wide, cudaStream_t s) {
     using Lay = sc::GradLayout<SP>;
     const size_t smem = (size_t)Lay::floats(a.L) * sizeof(float);
     const auto grad = a.pairs ? sc::ssm_grad_kernel<T, SP, true> : sc::ssm_grad_kernel<T, SP, false>;
-    cudaError_t e = cudaFuncSetAttribute(grad, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    // the largest any plan asks for: calls of different shapes may be on their way at once
+    cudaError_t e = cudaFuncSetAttribute(grad, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)(Lay::floats(sc::kMaxChunkBwd) * sizeof(float)));
     if (e == cudaSuccess && a.P > 1) {
         a.tiles = (a.D + sc::kThreads - 1) / sc::kThreads;
         e = walk_launch<T, SP, sc::kLocalBwd, 1>(a, wide, s);

@@ -15,6 +15,9 @@
 //     registers, then backward.
 // Each state element costs close to three exponentials and about 18 multiply-adds a token.  The
 // division by a_p that would spare the states' second run is not open: decays may be 0.
+// 4 x 1961 tokens of 1536 channels, 16 states: 406 us, of which ssm_grad_kernel 304 (257 instructions a
+// token and 16 channels, issued 59 % of the time by 12 warps an SM: instruction issue and its
+// latencies bound it, the exponentials' pipe is busy 32 %), the walk 85, the fold 22, the sums 13.
 //
 // Layout: a lane holds two neighbouring channels by four states.  The sums over channels (dB, dC:
 // 8 values a token) and over states (q, r, y: 6 values) are butterflies that halve the number
