@@ -14,12 +14,12 @@ struct ConvPlan {
     long long parts;    // chunks
     int tile;           // positions of a chunk
 };
-// Backward: chunks enough for one wave of eight blocks an SM (every block writes a partial row of the
-// parameters' sums), of 32 positions at least (each recomputes K - 1 more).
-static ConvPlan conv_bwd_plan(int B, long long N, int D) {
+// The walks: chunks enough for one wave of `blocks` blocks an SM (backward every block writes a partial
+// row of the parameters' sums), of 32 positions at least (each begins with K - 1 more).
+static ConvPlan conv_plan(int B, long long N, int D, int blocks) {
     ConvPlan p{};
     const long long blocks_c = (D + 127) / 128;
-    long long tiles = 148 * 8 / (blocks_c * B);
+    long long tiles = 148LL * blocks / (blocks_c * B);
     if (tiles < 1) tiles = 1;
     long long tile = (N + tiles - 1) / tiles;
     if (tile < 32) tile = 32;
@@ -28,6 +28,7 @@ static ConvPlan conv_bwd_plan(int B, long long N, int D) {
     p.parts = (long long)B * p.tiles;
     return p;
 }
+static ConvPlan conv_bwd_plan(int B, long long N, int D) { return conv_plan(B, N, D, 8); }
 
 static gtr_status_t check_conv(const gtr_conv_t *c) {
     if (c == nullptr || bad_common(c->B, c->Hgrid, c->Wgrid, c->D, c->direction, c->dtype)) return GTR_ERR_INVALID_ARG;
@@ -58,32 +59,47 @@ static cv::Args conv_args(const gtr_conv_t *c) {
     return a;
 }
 
-template <typename T, int V, int K, int TP>
-static cudaError_t conv_fwd_launch(cv::Args a, cudaStream_t s) {
+template <typename T, int V, int K>
+static cudaError_t conv_direct(cv::Args a, cudaStream_t s) {
     a.groups = (a.D + V - 1) / V;
-    a.tiles = (a.N + TP - 1) / TP;
+    a.tiles = (a.N + cv::kDirect - 1) / cv::kDirect;
     const long long blocks = ((long long)a.B * a.tiles * a.groups + cv::kThreads - 1) / cv::kThreads;
     if (blocks > kMaxGrid) return cudaErrorInvalidConfiguration;
-    return launch_after(cv::causal_conv_fwd_kernel<T, V, K, TP>, (unsigned)blocks, dim3(cv::kThreads), 0, s, a);
+    return launch_after(cv::causal_conv_fwd_kernel<T, V, K>, (unsigned)blocks, dim3(cv::kThreads), 0, s, a);
 }
-template <typename T, int V>
-static cudaError_t conv_fwd_k(const cv::Args &a, int K, cudaStream_t s) {
-    // four positions a thread instead of eight while eight make fewer than three blocks an SM
-    const bool few = (long long)a.B * ((a.N + 7) / 8) * ((a.D + V - 1) / V) < 148LL * 3 * cv::kThreads;
+template <typename T, int K>
+static cudaError_t conv_walk(cv::Args a, const ConvPlan &p, bool wide, cudaStream_t s) {
+    a.groups = (a.D + 2 * cv::kWalkThreads - 1) / (2 * cv::kWalkThreads);
+    a.tile = p.tile;
+    a.tiles = (int)p.tiles;
+    if (p.parts * a.groups > kMaxGrid) return cudaErrorInvalidConfiguration;
+    return launch_after(wide ? cv::causal_conv_walk_kernel<T, K, true> : cv::causal_conv_walk_kernel<T, K, false>,
+                        (unsigned)(p.parts * a.groups), dim3(cv::kWalkThreads), 0, s, a);
+}
+template <typename T, int K>
+static cudaError_t conv_fwd_launch(const cv::Args &a, bool wide, cudaStream_t s) {
+    // the walk once there are chunks of 32 positions for eight blocks an SM: fewer leave the machine to
+    // latency, which the direct kernel meets once a thread
+    if ((long long)a.B * ((a.N + 31) / 32) * ((a.D + 127) / 128) >= 148 * 8)
+        return conv_walk<T, K>(a, conv_plan(a.B, a.N, a.D, 10), wide, s);
+    return wide ? conv_direct<T, 8, K>(a, s) : conv_direct<T, 1, K>(a, s);
+}
+template <typename T>
+static cudaError_t conv_fwd_k(const cv::Args &a, int K, bool wide, cudaStream_t s) {
     switch (K) {
-    case 2: return few ? conv_fwd_launch<T, V, 2, 4>(a, s) : conv_fwd_launch<T, V, 2, 8>(a, s);
-    case 3: return few ? conv_fwd_launch<T, V, 3, 4>(a, s) : conv_fwd_launch<T, V, 3, 8>(a, s);
-    default: return few ? conv_fwd_launch<T, V, 4, 4>(a, s) : conv_fwd_launch<T, V, 4, 8>(a, s);
+    case 2: return conv_fwd_launch<T, 2>(a, wide, s);
+    case 3: return conv_fwd_launch<T, 3>(a, wide, s);
+    default: return conv_fwd_launch<T, 4>(a, wide, s);
     }
 }
 
 template <typename T, int K>
 static cudaError_t conv_bwd_launch(cv::Args a, const ConvPlan &p, bool wide, float *gw, float *gb, cudaStream_t s) {
-    a.groups = (a.D + 2 * cv::kBwdThreads - 1) / (2 * cv::kBwdThreads);
+    a.groups = (a.D + 2 * cv::kWalkThreads - 1) / (2 * cv::kWalkThreads);
     const long long blocks = p.parts * a.groups;
     if (blocks > kMaxGrid) return cudaErrorInvalidConfiguration;
     const cudaError_t e = launch_after(wide ? cv::causal_conv_bwd_kernel<T, K, true> : cv::causal_conv_bwd_kernel<T, K, false>,
-                                       (unsigned)blocks, dim3(cv::kBwdThreads), 0, s, a);
+                                       (unsigned)blocks, dim3(cv::kWalkThreads), 0, s, a);
     if (e != cudaSuccess) return e;
     const long long cols = (long long)(K + 1) * a.D;
     return launch_after(cv::causal_conv_sum_kernel<K>, (unsigned)((cols + 31) / 32), dim3(32, 8), 0, s,
@@ -125,9 +141,8 @@ extern "C" gtr_status_t gtr_causal_conv_fwd(const gtr_conv_t *conv, void *out, v
     const void *ps[] = {a.x, a.out, a.fin, a.init};
     const long long lds[] = {a.ldx};
     const bool wide = rows_on(16, a.D, ps, 4, lds, 1);
-    const bool h = conv->dtype == GTR_F16;
-    return ops_cuda_status(wide ? (h ? conv_fwd_k<__half, 8>(a, conv->K, s) : conv_fwd_k<__nv_bfloat16, 8>(a, conv->K, s))
-                                : (h ? conv_fwd_k<__half, 1>(a, conv->K, s) : conv_fwd_k<__nv_bfloat16, 1>(a, conv->K, s)));
+    return ops_cuda_status(conv->dtype == GTR_F16 ? conv_fwd_k<__half>(a, conv->K, wide, s)
+                                                  : conv_fwd_k<__nv_bfloat16>(a, conv->K, wide, s));
 }
 
 extern "C" size_t gtr_causal_conv_bwd_workspace_bytes(int B, int Hgrid, int Wgrid, int D, int K) {

@@ -140,6 +140,14 @@ __device__ __forceinline__ Raw<V> pack(const float (&f)[V]) {
     return r;
 }
 
+// Elements as float32 in pairs (V = 1: the element and a zero).
+template <typename T, int V>
+__device__ __forceinline__ void pairs_of(const Raw<V> &r, float2 (&f)[(V + 1) / 2]) {
+#pragma unroll
+    for (int i = 0; i < (V + 1) / 2; ++i)
+        f[i] = V == 1 ? make_float2(Elem<T>::get((uint16_t)r.w[0]), 0.f) : Elem<T>::get2(r.w[i]);
+}
+
 // ------------------------------------------------------------------ asynchronous copies
 // 16 bytes to shared memory; `bytes` of them (0 or 16) are read, the rest becomes zeros.
 __device__ __forceinline__ void copy16_async(void *dst, const void *src, uint32_t bytes) {

@@ -75,8 +75,9 @@ CONV = [
     (2, 37, 53, 70, 2, 3, "bf16", False, True, True),   # even channels, no whole 16 bytes
     (1, 1, 1000, 1, 3, 0, "bf16", True, False, False),  # one channel
     (1, 3, 67, 136, 2, 0, "fp16", True, True, True),
-    (2, 64, 64, 520, 4, 1, "fp16", True, True, True),   # blocks enough for eight positions a thread
-    (2, 64, 64, 67, 3, 2, "bf16", True, True, False),   # the same by single elements
+    (2, 64, 64, 520, 4, 1, "fp16", True, True, True),   # positions enough for the walk over chunks
+    (4, 64, 96, 130, 3, 1, "bf16", True, True, True),   # the same by single elements
+    (3, 1, 4099, 515, 2, 0, "fp16", False, False, True),
     (40, 5, 9, 384, 4, 3, "bf16", True, True, True),    # many short sequences
 ]
 
@@ -146,6 +147,18 @@ def test_conv_carried_state_equals_one_run():
                                        final_state=st)
         assert torch.equal(y, whole[:, lo:hi])
     assert torch.equal(st, wf)
+
+
+@pytest.mark.parametrize("B,N,D", [(3, 2, 48), (40, 64, 2048), (700, 2, 256), (400, 33, 257)])
+def test_conv_state_carried_in_place(B, N, D):
+    """final_state = init_state gives what two tensors give, bit for bit, directly and by chunks."""
+    dev = torch.device("cuda", 0)
+    _, d = conv_inputs(B, 1, N, D, 4, torch.float16, True, True, dev, seed=D)
+    out, fin = ssm.gtr_causal_conv_fwd(d["x"], d["w"], 1, N, 0, bias=d["b"], init_state=d["init"], final_state=True)
+    st = d["init"].clone()
+    got, _ = ssm.gtr_causal_conv_fwd(d["x"], d["w"], 1, N, 0, bias=d["b"], init_state=st, final_state=st)
+    assert torch.equal(got, out) and torch.equal(st, fin)
+    assert torch.equal(fin, torch.cat((d["init"], d["x"]), 1)[:, N:])
 
 
 # ------------------------------------------------------------------ selective scan
