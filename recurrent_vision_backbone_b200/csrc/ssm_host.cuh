@@ -64,10 +64,21 @@ inline int ssm_inputs(const gtr_ssm_t *m, const sc::Args &a, Span *s) {
     return n;
 }
 
+// How the states that a call lacks of SP are left out.
+template <int SP>
+inline sc::Pad state_padding(int S) { return S == SP ? sc::kFull : S % 4 == 0 ? sc::kQuads : sc::kAny; }
+template <typename T, int SP, int MODE, int SL, sc::Pad PAD>
+static auto walk_kernel(bool wide) {
+    return wide ? sc::ssm_walk_kernel<T, SP, MODE, true, SL, PAD> : sc::ssm_walk_kernel<T, SP, MODE, false, SL, PAD>;
+}
 template <typename T, int SP, int MODE, int SL>
 static cudaError_t walk_launch(const sc::Args &a, bool wide, cudaStream_t s) {
     const unsigned grid = (unsigned)((long long)a.tiles * a.B * (MODE == sc::kLocal ? a.P - 1 : a.P));
-    const auto kernel = wide ? sc::ssm_walk_kernel<T, SP, MODE, true, SL> : sc::ssm_walk_kernel<T, SP, MODE, false, SL>;
+    auto kernel = walk_kernel<T, SP, MODE, SL, sc::kFull>(wide);
+    if constexpr (MODE == sc::kOut) {
+        const sc::Pad pad = state_padding<SP>(a.S);
+        if (pad != sc::kFull) kernel = pad == sc::kQuads ? walk_kernel<T, SP, MODE, SL, sc::kQuads>(wide) : walk_kernel<T, SP, MODE, SL, sc::kAny>(wide);
+    }
     // A walk that opens a call and covers many SMs starts plainly: blocks that wait on SMs where the
     // call ahead happens to have left room end up unevenly spread (468 us for 428 at 8 x 2304 tokens of
     // 2048 channels)

@@ -56,6 +56,12 @@ struct Args {
 
 enum { kLocal = 0, kOut = 1, kLocalBwd = 2 };
 
+// States that only fill a kernel's, and how they stay out of the sums over states (their zeros times an
+// infinite step, input or gradient would be no number there).  kFull: there are none.  kQuads: S is
+// a multiple of four, whole groups of four are left out (backward 2 to 5 % of the time, forward none).
+// kAny: values are selected one by one (backward 10 to 14 % at 5 states).
+enum Pad { kFull = 0, kQuads = 1, kAny = 2 };
+
 __host__ __device__ constexpr int left_of(int nv, int lanes) { return nv > lanes ? nv / lanes : 1; }
 
 template <int MODE>
@@ -67,10 +73,12 @@ __host__ __device__ constexpr int walk_blocks() { return SP > 16 ? 1 : MODE == k
 
 // One walk over one chunk.  kLocal: hs[b][j] = the state reached from zero, sdt = the sum of the
 // time steps.  kLocalBwd: also gs[b][j] = sum_p (prod_{r <= p} a_r) C_p e_p, the gradient that
-// the chunk's outputs send to the state entering it.  kOut: outputs and the final state.
-template <typename T, int SP, int MODE, bool WIDE, int SL>
+// the chunk's outputs send to the state entering it.  kOut: outputs and the final state; the
+// other modes keep every state to itself, so that only kOut has to leave padded ones out.
+template <typename T, int SP, int MODE, bool WIDE, int SL, Pad PAD>
 __global__ void __launch_bounds__(kThreads, walk_blocks<SP, MODE, SL>()) ssm_walk_kernel(const Args a) {
     static_assert(SL == 1 || (SL == 2 && MODE == kOut), "the local walks have chunks enough");
+    static_assert(PAD == kFull || MODE == kOut, "only the outputs sum over states");
     constexpr int CH = kThreads / SL;           // channels of the block
     constexpr int TOK = 8 * SL;                 // tokens of a tile
     constexpr int NP = SP / SL / 2;             // pairs of states of a lane
@@ -190,6 +198,11 @@ __global__ void __launch_bounds__(kThreads, walk_blocks<SP, MODE, SL>()) ssm_wal
         float2 y0 = splat(0.f), y1 = splat(0.f);
 #pragma unroll
         for (int q = 0; q < NP / 2; ++q) {
+            // with one lane a channel the first half of the states are never padded, and the group is passed
+            // over; with two, where only the second lane would, it only leaves the sum (passing over it:
+            // 378 us for 285 at 8 x 2304 tokens of 2048 channels, 12 states)
+            const bool maybe = SL > 1 || 4 * q >= SP / 2, in = PAD != kQuads || !maybe || n0 + 4 * q < a.S;
+            if (SL == 1 && !in) break;
             const float4 Bq = B4[q];
             const float4 Cq = MODE != kLocal ? C4[q] : Bq;
 #pragma unroll
@@ -199,7 +212,9 @@ __global__ void __launch_bounds__(kThreads, walk_blocks<SP, MODE, SL>()) ssm_wal
                 const float2 m = __fmul2_rn(t2, A2[k]);
                 const float2 d = make_float2(ex2(m.x), ex2(m.y));
                 h[k] = __ffma2_rn(d, h[k], __fmul2_rn(x2, Bk));
-                if (MODE == kOut) (k & 1 ? y1 : y0) = __ffma2_rn(Ck, h[k], k & 1 ? y1 : y0);
+                if (PAD == kAny && maybe)
+                    h[k] = make_float2(n0 + 2 * k < a.S ? h[k].x : 0.f, n0 + 2 * k + 1 < a.S ? h[k].y : 0.f);
+                if (MODE == kOut && (SL == 1 || in)) (k & 1 ? y1 : y0) = __ffma2_rn(Ck, h[k], k & 1 ? y1 : y0);
                 if (MODE == kLocalBwd) {
                     pr[k] = __fmul2_rn(pr[k], d);
                     g[k] = __ffma2_rn(pr[k], __fmul2_rn(e2, Ck), g[k]);

@@ -42,11 +42,17 @@ static ScanBwdWs scan_bwd_ws(int B, long long N, int D, int S, const BwdPlan &p)
     return w;
 }
 
+template <typename T, int SP, sc::Pad PAD>
+static auto grad_kernel(bool pairs) {
+    return pairs ? sc::ssm_grad_kernel<T, SP, true, PAD> : sc::ssm_grad_kernel<T, SP, false, PAD>;
+}
 template <typename T, int SP>
 static cudaError_t scan_bwd_launch(sc::Args a, bool wide, cudaStream_t s) {
     using Lay = sc::GradLayout<SP>;
     const size_t smem = (size_t)Lay::floats(a.L) * sizeof(float);
-    const auto grad = a.pairs ? sc::ssm_grad_kernel<T, SP, true> : sc::ssm_grad_kernel<T, SP, false>;
+    const sc::Pad pad = a.S % 4 != 0 ? sc::kAny : a.S == SP && a.D % Lay::CT == 0 ? sc::kFull : sc::kQuads;
+    const auto grad = pad == sc::kFull ? grad_kernel<T, SP, sc::kFull>(a.pairs)
+                      : pad == sc::kQuads ? grad_kernel<T, SP, sc::kQuads>(a.pairs) : grad_kernel<T, SP, sc::kAny>(a.pairs);
     // the largest any plan asks for: calls of different shapes may be on their way at once
     cudaError_t e = cudaFuncSetAttribute(grad, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)(Lay::floats(sc::kMaxChunkBwd) * sizeof(float)));

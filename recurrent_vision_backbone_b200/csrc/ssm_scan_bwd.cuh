@@ -37,14 +37,20 @@ struct GradLayout {
     static constexpr int CW = 64 / SL;           // channels of a warp
     static constexpr int CT = 4 * CW;            // channels of a block
     static constexpr int NE = (kSub * CW / 2 + 31) / 32;   // (token, channel pair) entries a lane prepares
-    // shared memory, floats: B, C of the chunk; checkpoints; per warp t, x, e and q, r, y; dB, dC
+    // shared memory, floats: B, C of the chunk; checkpoints; per warp t, x, e and q, r, y; dB, dC; zeros
+    // for the lanes that hold nothing, 16 banks away from what the others read with them
     static constexpr int stage = 6 * kSub * CW;
+    static constexpr int zeros = kSub * (3 * CW > SP ? 3 * CW : SP);
     static __host__ __device__ constexpr int floats(int L) {
-        return 2 * L * SP + L / kSub * kThreads * 8 + 4 * stage + 2 * 4 * kSub * 2 * SP;
+        return 2 * L * SP + L / kSub * kThreads * 8 + 4 * stage + 2 * 4 * kSub * 2 * SP + 16 + zeros;
     }
 };
 
-template <typename T, int SP, bool PAIRS>   // PAIRS: rows of channels start on 4 bytes and are even
+// PAIRS: rows of channels start on 4 bytes and are even.  PAD also covers the channels that only fill a
+// block's (the sums over channels take them in): a lane without a state or a channel of the
+// call's reads zeros for t, x, e, B and C, the second channel of an odd row's last pair is left out
+// of its lane's sums.
+template <typename T, int SP, bool PAIRS, Pad PAD>
 __global__ void __launch_bounds__(kThreads, 3) ssm_grad_kernel(const Args a) {
     using Lay = GradLayout<SP>;
     constexpr int SL = Lay::SL, CW = Lay::CW, NE = Lay::NE;
@@ -70,7 +76,19 @@ __global__ void __launch_bounds__(kThreads, 3) ssm_grad_kernel(const Args a) {
     const int c = cb + 2 * pr;                   // this lane's channels: c, c + 1
     const bool cv[2] = {c < a.D, c + 1 < a.D};
     const bool gate = a.z != nullptr, sp_on = a.softplus != 0;
+    const bool live = PAD != kQuads || (cv[0] && sl * 4 < a.S);
+    const bool two = PAD == kFull || PAIRS || cv[1];
+    float *zeros = wsum + 2 * 4 * kSub * 2 * SP + 16;
+    // what this lane reads of a token: its channels' t, x, e, its states' B and C
+    auto pair_of = [&](const float *p, int tt) {
+        return *reinterpret_cast<const float2 *>(live ? p + tt * CW + 2 * pr : zeros + (p - st) + tt * CW);
+    };
+    auto quad_of = [&](const float *p, int s, int tt) {
+        return *reinterpret_cast<const float4 *>(live ? p + (s * kSub + tt) * SP + sl * 4 : zeros + tt * SP);
+    };
 
+    if (PAD == kQuads)
+        for (int i = tid; i < Lay::zeros; i += kThreads) zeros[i] = 0.f;
     if (tid < p1 - p0) stok[tid] = token_of(p0 + tid, a.H, a.W, a.dir);
     __syncthreads();
     for (int i = tid; i < (p1 - p0) * SP; i += kThreads) {
@@ -156,12 +174,17 @@ __global__ void __launch_bounds__(kThreads, 3) ssm_grad_kernel(const Args a) {
         if (PAIRS) copy_wait<kAhead - 1>();
         return raw[k % (kAhead + 1)];
     };
+    auto real = [&](int k, int i, float2 v) {   // kAny: 0 where pair i of channel k only fills the lane
+        if (PAD != kAny) return v;
+        const int n = sl * 4 + 2 * i;
+        return make_float2(cv[k] && n < a.S ? v.x : 0.f, cv[k] && n + 1 < a.S ? v.y : 0.f);
+    };
     auto put2 = [](float *p, float2 v) { *reinterpret_cast<float2 *>(p) = v; };
     // a token forward: the decays, and the states after it
     auto forward = [&](int s, int tt, float2 (&d)[2][2]) {
-        const float2 t = *reinterpret_cast<const float2 *>(st + tt * CW + 2 * pr);
-        const float2 x = *reinterpret_cast<const float2 *>(sx + tt * CW + 2 * pr);
-        const float4 B = *reinterpret_cast<const float4 *>(sB + (s * kSub + tt) * SP + sl * 4);
+        const float2 t = pair_of(st, tt);
+        const float2 x = pair_of(sx, tt);
+        const float4 B = quad_of(sB, s, tt);
         const float2 Bv[2] = {make_float2(B.x, B.y), make_float2(B.z, B.w)};
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
@@ -169,8 +192,8 @@ __global__ void __launch_bounds__(kThreads, 3) ssm_grad_kernel(const Args a) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const float2 m = __fmul2_rn(tk, A2[k][i]);
-                d[k][i] = make_float2(ex2(m.x), ex2(m.y));
-                h[k][i] = __ffma2_rn(d[k][i], h[k][i], __fmul2_rn(xk, Bv[i]));
+                d[k][i] = real(k, i, make_float2(ex2(m.x), ex2(m.y)));
+                h[k][i] = real(k, i, __ffma2_rn(d[k][i], h[k][i], __fmul2_rn(xk, Bv[i])));
             }
         }
     };
@@ -249,11 +272,11 @@ __global__ void __launch_bounds__(kThreads, 3) ssm_grad_kernel(const Args a) {
 #pragma unroll
         for (int tt = kSub - 1; tt >= 0; --tt) {
             if (!FULL && tt >= m) continue;
-            const float2 t = *reinterpret_cast<const float2 *>(st + tt * CW + 2 * pr);
-            const float2 x = *reinterpret_cast<const float2 *>(sx + tt * CW + 2 * pr);
-            const float2 e = *reinterpret_cast<const float2 *>(se + tt * CW + 2 * pr);
-            const float4 B = *reinterpret_cast<const float4 *>(sB + (q0 + tt) * SP + sl * 4);
-            const float4 C = *reinterpret_cast<const float4 *>(sC + (q0 + tt) * SP + sl * 4);
+            const float2 t = pair_of(st, tt);
+            const float2 x = pair_of(sx, tt);
+            const float2 e = pair_of(se, tt);
+            const float4 B = quad_of(sB, s, tt);
+            const float4 C = quad_of(sC, s, tt);
             const float2 Bv[2] = {make_float2(B.x, B.y), make_float2(B.z, B.w)};
             const float2 Cv[2] = {make_float2(C.x, C.y), make_float2(C.z, C.w)};
             float2 vb[2], vc[2];                           // dB, dC of this lane's channels
@@ -265,14 +288,16 @@ __global__ void __launch_bounds__(kThreads, 3) ssm_grad_kernel(const Args a) {
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     const float2 hn = tt + 1 < kSub ? hp[tt + 1 < kSub ? tt + 1 : tt][k][i] : h[k][i];   // after the token
-                    const float2 G = __ffma2_rn(ek, Cv[i], g[k][i]);
+                    const float2 G = real(k, i, __ffma2_rn(ek, Cv[i], g[k][i]));
                     const float2 Ga = __fmul2_rn(G, d[tt][k][i]), w = __fmul2_rn(Ga, hp[tt][k][i]);
                     q = __ffma2_rn(G, Bv[i], q);
                     r = __ffma2_rn(w, A2[k][i], r);
                     y = __ffma2_rn(Cv[i], hn, y);
                     dA[k][i] = __ffma2_rn(w, tk, dA[k][i]);
-                    vb[i] = k ? __ffma2_rn(G, xk, vb[i]) : __fmul2_rn(G, xk);
-                    vc[i] = k ? __ffma2_rn(ek, hn, vc[i]) : __fmul2_rn(ek, hn);
+                    if (k == 0)
+                        vb[i] = __fmul2_rn(G, xk), vc[i] = __fmul2_rn(ek, hn);
+                    else if (two)
+                        vb[i] = __ffma2_rn(G, xk, vb[i]), vc[i] = __ffma2_rn(ek, hn, vc[i]);
                     g[k][i] = Ga;
                 }
                 vs[k] = q.x + q.y;
