@@ -30,10 +30,11 @@ struct Args {
     int tile, tiles;                // positions of a thread or chunk, their number a sequence
 };
 
-// Row r of X (r counts from the K - 1 earlier inputs) at channels c .. c + V - 1.
+// Row r < K - 1 of X, an earlier input, at channels c .. c + V - 1.  final_state may be init_state, so these
+// are plain loads: each thread has the rows it needs before it writes any.
 template <int V>
 __device__ __forceinline__ Raw<V> early_row(const Args &a, int b, int r, int K, int c) {
-    return a.init != nullptr ? load_raw<V>(a.init + ((long long)b * (K - 1) + r) * a.D + c) : zero_raw<V>();
+    return a.init != nullptr ? load_plain<V>(a.init + ((long long)b * (K - 1) + r) * a.D + c) : zero_raw<V>();
 }
 
 // Few positions.  One thread: V channels, kDirect consecutive scan positions; every row it needs
@@ -92,8 +93,8 @@ __global__ void __launch_bounds__(kThreads, 4) causal_conv_fwd_kernel(const Args
 #pragma unroll
     for (int v = 0; v < NP; ++v)
         bias[v] = a.bias != nullptr ? make_float2(__ldg(a.bias + c + 2 * v), V == 1 ? 0.f : __ldg(a.bias + c + 2 * v + (V > 1))) : splat(0.f);
-    // tile 0 also writes the carried rows: the last K - 1 of X.  The rows it needs of
-    // init_state are in registers by then, so final_state may be init_state
+    // tile 0 also writes the carried rows: the last K - 1 of X, after it has read what it needs of init_state
+    // (which no other tile reads)
     if (tile == 0 && a.fin != nullptr) {
         Raw<V> f[K - 1];
 #pragma unroll
@@ -147,7 +148,7 @@ static_assert(kTok * kRowThreads == 2 * kWalkThreads, "two rows of a tile a thre
 // Eight channels of a finished row to memory, `left` of them inside the tensor.
 template <typename T, bool WIDE>
 __device__ __forceinline__ bool put_row(uint16_t *dst, const uint16_t *src, int left) {
-    const Raw<8> v = load_raw_shared(src);
+    const Raw<8> v = load_plain<8>(src);
     if (WIDE) {
         store_raw<8>(dst, v);
         return Elem<T>::bad_raw(Elem<T>::worst(Elem<T>::worst(v.w[0], v.w[1]), Elem<T>::worst(v.w[2], v.w[3])));
@@ -169,10 +170,13 @@ __device__ __forceinline__ float2 param_pair(const float *p, int c, bool v0, boo
 // Row r of X at channels c, c + 1 (r counts from the K - 1 earlier inputs).
 template <typename T, int K>
 __device__ __forceinline__ float2 row_pair(const Args &a, int b, int r, int c, bool v0, bool v1) {
-    const uint16_t *src = r >= K - 1 ? a.x + ((long long)b * a.N + token_of(r - (K - 1), a.H, a.W, a.dir)) * a.ldx + c
-                          : a.init != nullptr ? a.init + ((long long)b * (K - 1) + r) * a.D + c : nullptr;
-    return make_float2(src != nullptr && v0 ? Elem<T>::get(__ldg(src)) : 0.f,
-                       src != nullptr && v1 ? Elem<T>::get(__ldg(src + 1)) : 0.f);
+    if (r < K - 1) {   // plain loads, see early_row
+        if (a.init == nullptr) return splat(0.f);
+        const uint16_t *e = a.init + ((long long)b * (K - 1) + r) * a.D + c;
+        return make_float2(v0 ? Elem<T>::get(e[0]) : 0.f, v1 ? Elem<T>::get(e[1]) : 0.f);
+    }
+    const uint16_t *src = a.x + ((long long)b * a.N + token_of(r - (K - 1), a.H, a.W, a.dir)) * a.ldx + c;
+    return make_float2(Elem<T>::get(ld16(src, v0)), Elem<T>::get(ld16(src + 1, v1)));
 }
 
 // Many positions.  A thread walks its chunk with the last K rows of X in registers; rows come two
@@ -221,7 +225,7 @@ __global__ void __launch_bounds__(kWalkThreads, 10) causal_conv_walk_kernel(cons
     const float2 bias = param_pair(a.bias, c, v0, v1, 0, 1);
 #pragma unroll
     for (int j = 0; j < K - 1; ++j) xw[j] = row_pair<T, K>(a, b, p0 + j, c, v0, v1);
-    if (chunk == 0 && a.fin != nullptr) {   // the carried rows: the rows of init_state are in registers by then
+    if (chunk == 0 && a.fin != nullptr) {   // the carried rows, after the thread's reads of init_state
         float2 f[K - 1];
 #pragma unroll
         for (int j = 0; j < K - 1; ++j) f[j] = row_pair<T, K>(a, b, a.N + j, c, v0, v1);

@@ -85,6 +85,9 @@ template <int V>
 struct Raw {
     uint32_t w[V >= 2 ? V / 2 : 1];
 };
+// load_raw goes through the read-only path: not for memory that the same kernel writes.  (What the launch
+// ahead wrote may be read so: nothing of it is asked for before chain_wait, behind which all of
+// that launch's writes are visible, and it does not change any more.)
 template <int V>
 __device__ __forceinline__ Raw<V> load_raw(const uint16_t *p) {
     Raw<V> r;
@@ -97,9 +100,15 @@ __device__ __forceinline__ Raw<V> load_raw(const uint16_t *p) {
     }
     return r;
 }
-__device__ __forceinline__ Raw<8> load_raw_shared(const uint16_t *p) {
-    const uint4 x = *reinterpret_cast<const uint4 *>(p);
-    return {{x.x, x.y, x.z, x.w}};
+template <int V>
+__device__ __forceinline__ Raw<V> load_plain(const uint16_t *p) {
+    if constexpr (V == 8) {
+        const uint4 x = *reinterpret_cast<const uint4 *>(p);
+        return {{x.x, x.y, x.z, x.w}};
+    } else {
+        static_assert(V == 1, "16 or 2 bytes");
+        return {{*p}};
+    }
 }
 template <int V>
 __device__ __forceinline__ void store_raw(uint16_t *p, const Raw<V> &r) {

@@ -140,7 +140,7 @@ __global__ void __launch_bounds__(kThreads, walk_blocks<SP, MODE, SL>()) ssm_wal
     bool bad = false;
     auto flush = [&](int pb, int n, int buf) {
         if (pb + tt >= p1 || left <= 0) return;
-        const Raw<8> r = load_raw_shared(&outs[buf][MODE == kOut ? tt : 0][MODE == kOut ? tc * 8 : 0]);
+        const Raw<8> r = load_plain<8>(&outs[buf][MODE == kOut ? tt : 0][MODE == kOut ? tc * 8 : 0]);
         uint16_t *dst = a.out + (row0 + n) * a.D + c8;
         if (WIDE) {   // whole pieces
             bad |= Elem<T>::bad_raw(Elem<T>::worst(Elem<T>::worst(r.w[0], r.w[1]), Elem<T>::worst(r.w[2], r.w[3])));
