@@ -7,6 +7,8 @@
 //     grad_gamma = sum_b Q,  grad_beta = sum_b P
 // A few operations for 4 bytes moved (6 backward): HBM-bound, and what costs is reading the
 // activations once for the sums and again for the result.
+#include <type_traits>
+
 #include "../../include/gtr_norm.h"
 #include "ops_common.cuh"
 
@@ -299,11 +301,11 @@ __global__ void __launch_bounds__(32 * kLanes, 3) group_norm_results_kernel(cons
     const bool live = x < pc.n;
     const long long base = (long long)b * a.N * a.C + c;
     Raw<8> rx[AT], rd[AT], nx[AT], nd[AT];
-    auto fetch = [&](int r) {
+    auto fetch = [&](int r) {   // x by plain loads: out may be x
 #pragma unroll
         for (int u = 0; u < AT; ++u) {
             const bool in = live && r + u * kLanes < r1;
-            nx[u] = in ? load_raw<8>(a.x + base + (long long)(r + u * kLanes) * a.C) : zero_raw<8>();
+            nx[u] = in ? load_plain<8>(a.x + base + (long long)(r + u * kLanes) * a.C) : zero_raw<8>();
             if (BWD) nd[u] = in ? load_raw<8>(a.dy + base + (long long)(r + u * kLanes) * a.C) : zero_raw<8>();
         }
     };
@@ -572,24 +574,39 @@ __global__ void __launch_bounds__(32 * kRowLanes) group_norm_apply_kernel(const 
         if (BWD) k1[v] = a.coef[2 * g], k2[v] = a.coef[2 * g + 1];
     }
     bool bad = false;
-#pragma unroll 4
-    for (int r = r0 + threadIdx.y; r < r1; r += kRowLanes) {
-        float x[V], y[V], dy[V];
-        unpack<T, V>(load_raw<V>(a.x + base + (long long)r * a.C), x);
-        if (BWD) unpack<T, V>(load_raw<V>(a.dy + base + (long long)r * a.C), dy);
+    // `count` rows from r on, asked for at once: x by plain loads, since out may be x forward, so that a load
+    // stays ahead of the stores behind it
+    auto rows = [&](auto count, int r) {
+        constexpr int AT = decltype(count)::value;
+        Raw<V> rx[AT], rd[AT];
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const float xh = (x[v] - mean[v]) * rstd[v], z = fmaf(xh, gam[v], bet[v]);
-            if (BWD) {
-                const float dz = a.act == GTR_ACT_SILU ? dy[v] * act_grad(z) : dy[v];
-                y[v] = rstd[v] * (fmaf(gam[v], dz, -k1[v]) - xh * k2[v]);
-            } else {
-                y[v] = a.act == GTR_ACT_SILU ? z * sigmoid_f(z) : z;
-            }
-            bad |= Elem<T>::bad(y[v]);
+        for (int u = 0; u < AT; ++u) {
+            const long long at = base + (long long)(r + u * kRowLanes) * a.C;
+            rx[u] = load_plain<V>(a.x + at);
+            if (BWD) rd[u] = load_raw<V>(a.dy + at);
         }
-        store_raw<V>(a.out + base + (long long)r * a.C, pack<T, V>(y));
-    }
+#pragma unroll
+        for (int u = 0; u < AT; ++u) {
+            float x[V], y[V], dy[V];
+            unpack<T, V>(rx[u], x);
+            if (BWD) unpack<T, V>(rd[u], dy);
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const float xh = (x[v] - mean[v]) * rstd[v], z = fmaf(xh, gam[v], bet[v]);
+                if (BWD) {
+                    const float dz = a.act == GTR_ACT_SILU ? dy[v] * act_grad(z) : dy[v];
+                    y[v] = rstd[v] * (fmaf(gam[v], dz, -k1[v]) - xh * k2[v]);
+                } else {
+                    y[v] = a.act == GTR_ACT_SILU ? z * sigmoid_f(z) : z;
+                }
+                bad |= Elem<T>::bad(y[v]);
+            }
+            store_raw<V>(a.out + base + (long long)(r + u * kRowLanes) * a.C, pack<T, V>(y));
+        }
+    };
+    int r = r0 + threadIdx.y;
+    for (; r + 3 * kRowLanes < r1; r += 4 * kRowLanes) rows(std::integral_constant<int, 4>{}, r);
+    for (; r < r1; r += kRowLanes) rows(std::integral_constant<int, 1>{}, r);
     if (bad) set_error(kOpsErrRange);
 }
 

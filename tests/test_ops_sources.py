@@ -6,6 +6,8 @@ tensor that a call may name as input and output at once is read by plain loads."
 import os
 import re
 
+import pytest
+
 CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "recurrent_vision_backbone_b200", "csrc")
 
 
@@ -13,6 +15,17 @@ def source(name):
     with open(os.path.join(CSRC, name)) as f:
         text = f.read()
     return re.sub(r"//[^\n]*", "", text)
+
+
+def body(text, name):
+    """The function or kernel `name` with its braces."""
+    i = text.index("{", re.search(r"\b%s\(" % name, text).end())
+    depth, j = 0, i
+    while True:
+        depth += {"{": 1, "}": -1}.get(text[j], 0)
+        j += 1
+        if depth == 0:
+            return text[i:j]
 
 
 def read_only_loads(text):
@@ -35,3 +48,11 @@ def test_carried_rows_of_the_convolution():
     loads = read_only_loads(text)
     for name in ["a.init"] + re.findall(r"\*\s*(\w+)\s*=[^;]*a\.init\b", text):
         assert not [a for a in loads if re.search(r"(?<![\w.])%s\b" % re.escape(name), a)], name
+
+
+@pytest.mark.parametrize("kernel", ["group_norm_results_kernel", "group_norm_apply_kernel"])
+def test_rows_of_a_norm_in_place(kernel):
+    """out may be x: the kernels that write out read x by plain loads."""
+    loads = read_only_loads(body(source("group_norm.cu"), kernel))
+    assert loads   # the parameters
+    assert not [a for a in loads if re.search(r"(?<![\w.])a\.x\b", a)]
