@@ -573,7 +573,7 @@ __global__ void __launch_bounds__(32 * kRowLanes) group_norm_apply_kernel(const 
         bet[v] = a.beta != nullptr ? __ldg(a.beta + c + v) : 0.f;
         if (BWD) k1[v] = a.coef[2 * g], k2[v] = a.coef[2 * g + 1];
     }
-    bool bad = false;
+    uint32_t worst = 0;
     // `count` rows from r on, asked for at once: x by plain loads, since out may be x forward, so that a load
     // stays ahead of the stores behind it
     auto rows = [&](auto count, int r) {
@@ -599,15 +599,17 @@ __global__ void __launch_bounds__(32 * kRowLanes) group_norm_apply_kernel(const 
                 } else {
                     y[v] = a.act == GTR_ACT_SILU ? z * sigmoid_f(z) : z;
                 }
-                bad |= Elem<T>::bad(y[v]);
             }
-            store_raw<V>(a.out + base + (long long)(r + u * kRowLanes) * a.C, pack<T, V>(y));
+            const Raw<V> o = pack<T, V>(y);
+#pragma unroll
+            for (const uint32_t w : o.w) worst = Elem<T>::worst(worst, w);
+            store_raw<V>(a.out + base + (long long)(r + u * kRowLanes) * a.C, o);
         }
     };
     int r = r0 + threadIdx.y;
     for (; r + 3 * kRowLanes < r1; r += 4 * kRowLanes) rows(std::integral_constant<int, 4>{}, r);
     for (; r < r1; r += kRowLanes) rows(std::integral_constant<int, 1>{}, r);
-    if (bad) set_error(kOpsErrRange);
+    if (Elem<T>::bad_raw(worst)) set_error(kOpsErrRange);
 }
 
 }  // namespace gn

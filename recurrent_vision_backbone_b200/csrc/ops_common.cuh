@@ -51,10 +51,8 @@ struct Elem<__half> {
         const __half2 h = __floats2half2_rn(a, b);
         return *reinterpret_cast<const uint32_t *>(&h);
     }
-    // whether a result left the type's range (|f| above the largest fp16, or NaN); the
-    // running maximum of |f| is what is tested, which fmaxf would lose a NaN from
-    static __device__ __forceinline__ bool bad(float f) { return !(fabsf(f) <= 65504.f); }
-    // the same of rounded values, two to a word (or one): an exponent of all ones
+    // whether a result left the type's range, tested on the rounded values, two to a word (or one): an
+    // exponent of all ones, an infinity or NaN (so every kernel draws the line at the same value, 65520)
     static __device__ __forceinline__ bool bad_raw(uint32_t w) {
         return (w & 0x7c00u) == 0x7c00u || (w & 0x7c000000u) == 0x7c000000u;
     }
@@ -75,8 +73,7 @@ struct Elem<__nv_bfloat16> {
         const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
         return *reinterpret_cast<const uint32_t *>(&h);
     }
-    static __device__ __forceinline__ bool bad(float) { return false; }   // bf16 holds what float32 holds
-    static __device__ __forceinline__ bool bad_raw(uint32_t) { return false; }
+    static __device__ __forceinline__ bool bad_raw(uint32_t) { return false; }   // bf16 holds what float32 holds
     static __device__ __forceinline__ uint32_t worst(uint32_t, uint32_t) { return 0; }
 };
 

@@ -437,8 +437,9 @@ __global__ void __launch_bounds__(256, NB <= 4 ? 4 : 2) ssm_token_kernel(const A
     if (mine && (NB > 1 || q == 0)) {
         float o = fmaf(Dk, u, y[0]);
         if (a.z != nullptr) o *= z * sigmoid_f(z);
-        a.out[bo * a.D + c] = Elem<T>::put(o);
-        if (Elem<T>::bad(o)) set_error(kOpsErrRange);
+        const uint16_t r = Elem<T>::put(o);
+        a.out[bo * a.D + c] = r;
+        if (Elem<T>::bad_raw(r)) set_error(kOpsErrRange);
     }
 }
 

@@ -398,8 +398,9 @@ __global__ void __launch_bounds__(256) ssm_grad_sum_kernel(const Args a, int bc_
         float s = 0.f;
 #pragma unroll 8
         for (int k = 0; k < a.tiles; ++k) s += a.pbc[((long long)k * rows + row) * 2 * SP + v];
-        (v < SP ? a.dB : a.dC)[row * a.S + n] = Elem<T>::put(s);
-        if (Elem<T>::bad(s)) set_error(kOpsErrRange);
+        const uint16_t r = Elem<T>::put(s);
+        (v < SP ? a.dB : a.dC)[row * a.S + n] = r;
+        if (Elem<T>::bad_raw(r)) set_error(kOpsErrRange);
         return;
     }
     const long long cols = (long long)a.D * (SP + 2);
