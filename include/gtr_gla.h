@@ -221,10 +221,12 @@ gtr_status_t gtr_gla_fwd_static(const gtr_half_t *q, const gtr_half_t *k, const 
                                 void *stream);
 
 /*
- * Syncs `stream`, then reads and clears the device error word (and any sticky
- * CUDA error).  Returns GTR_OK, GTR_ERR_TIMEOUT, GTR_ERR_RANGE or GTR_ERR_CUDA.  On
- * GTR_ERR_TIMEOUT it also zero-fills the library's workspaces of the current
- * device (the cached one and the static scratch).
+ * Syncs `stream`, then reads and clears the device error words of the current device: this
+ * header's and those of the operators in gtr_ssm.h and gtr_norm.h (and any sticky CUDA
+ * error).  Each word is read and cleared in one step, so that what kernels of other streams
+ * record meanwhile is reported by this call or by the next.  Returns GTR_OK,
+ * GTR_ERR_TIMEOUT, GTR_ERR_RANGE or GTR_ERR_CUDA.  On GTR_ERR_TIMEOUT it also zero-fills the
+ * library's workspaces of the current device (the cached one and the static scratch).
  */
 gtr_status_t gtr_gla_device_status(void *stream);
 

@@ -5,7 +5,7 @@
 
 namespace gtr {
 
-unsigned conv_take_errors() { return take_errors(); }
+unsigned *conv_error_word() { return error_word(); }
 
 using namespace ops;
 

@@ -614,7 +614,7 @@ __global__ void __launch_bounds__(32 * kRowLanes) group_norm_apply_kernel(const 
 
 }  // namespace gn
 
-unsigned norm_take_errors() { return take_errors(); }
+unsigned *norm_error_word() { return error_word(); }
 
 // ------------------------------------------------------------------ host
 using namespace ops;

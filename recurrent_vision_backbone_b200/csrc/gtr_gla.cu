@@ -999,6 +999,36 @@ extern "C" gtr_status_t gtr_gla_selftest_timeout(unsigned limit_us, void *stream
     return cuda_status(cudaGetLastError());
 }
 
+namespace gtr {
+
+// The error words of this file and of the operators', read and cleared in one step each: a bit that a
+// kernel of another stream sets meanwhile is seen by this call or by the next one.
+constexpr int kErrorWords = 5;
+struct ErrorWords {
+    unsigned *w[kErrorWords];
+};
+__device__ unsigned int g_taken_errors;
+__global__ void take_errors_kernel(ErrorWords e) {
+    unsigned word = 0;
+    for (int i = 0; i < kErrorWords; ++i) word |= atomicExch(e.w[i], 0u);
+    g_taken_errors = word;
+}
+static cudaError_t take_errors(unsigned *word) {
+    void *own = nullptr;
+    const cudaError_t sym = cudaGetSymbolAddress(&own, g_error_word);
+    if (sym != cudaSuccess) return sym;
+    const ErrorWords e{{static_cast<unsigned *>(own), conv_error_word(), ssm_error_word(), ssm_bwd_error_word(), norm_error_word()}};
+    for (unsigned *w : e.w)
+        if (w == nullptr) return cudaErrorInvalidSymbol;
+    static std::mutex mu;   // one g_taken_errors a device
+    std::lock_guard<std::mutex> lk(mu);
+    take_errors_kernel<<<1, 1, 0, cudaStreamLegacy>>>(e);
+    const cudaError_t launch = cudaGetLastError();
+    return launch != cudaSuccess ? launch : cudaMemcpyFromSymbol(word, g_taken_errors, sizeof(*word));
+}
+
+}  // namespace gtr
+
 extern "C" gtr_status_t gtr_gla_device_status(void *stream) {
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (cudaStreamSynchronize(s) != cudaSuccess) {
@@ -1006,18 +1036,12 @@ extern "C" gtr_status_t gtr_gla_device_status(void *stream) {
         return GTR_ERR_CUDA;
     }
     unsigned word = 0;
-    if (cudaMemcpyFromSymbol(&word, g_error_word, sizeof(word)) != cudaSuccess) return GTR_ERR_CUDA;
-    const unsigned ops_word = conv_take_errors() | ssm_take_errors() | ssm_bwd_take_errors() | norm_take_errors();   // read and cleared
-    if (ops_word & kOpsErrCuda) return GTR_ERR_CUDA;
-    word |= ops_word;
-    if (word == kErrRange) {
-        const unsigned zero = 0;
-        cudaMemcpyToSymbol(g_error_word, &zero, sizeof(zero));
-        return GTR_ERR_RANGE;
+    if (take_errors(&word) != cudaSuccess) {
+        cudaGetLastError();
+        return GTR_ERR_CUDA;
     }
+    if (word == kErrRange) return GTR_ERR_RANGE;
     if (word != 0) {
-        const unsigned zero = 0;
-        cudaMemcpyToSymbol(g_error_word, &zero, sizeof(zero));
         // a span launch that timed out can leave publish flags set: clear the library's
         // workspaces of this device (cached and static) so the next call starts from zero
         const int dev = current_device();

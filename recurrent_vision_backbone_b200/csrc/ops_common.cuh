@@ -18,14 +18,9 @@ namespace gtr {
 // The error word of this source file's kernels.
 static __device__ unsigned int g_ops_error_word;
 static __device__ __forceinline__ void set_error(unsigned e) { atomicOr(&g_ops_error_word, e); }
-static inline unsigned take_errors() {
-    unsigned word = 0;
-    if (cudaMemcpyFromSymbol(&word, g_ops_error_word, sizeof(word)) != cudaSuccess) return kOpsErrCuda;
-    if (word != 0) {
-        const unsigned zero = 0;
-        if (cudaMemcpyToSymbol(g_ops_error_word, &zero, sizeof(zero)) != cudaSuccess) return kOpsErrCuda;
-    }
-    return word;
+static inline unsigned *error_word() {   // its address on the current device; null: a CUDA error
+    void *p = nullptr;
+    return cudaGetSymbolAddress(&p, g_ops_error_word) == cudaSuccess ? static_cast<unsigned *>(p) : nullptr;
 }
 
 namespace ops {

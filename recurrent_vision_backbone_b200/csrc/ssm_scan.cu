@@ -7,7 +7,7 @@
 
 namespace gtr {
 
-unsigned ssm_take_errors() { return take_errors(); }
+unsigned *ssm_error_word() { return error_word(); }
 
 constexpr int kSmAim = 148 * 4;   // blocks of four warps that keep the schedulers busy
 

@@ -7,7 +7,7 @@
 
 namespace gtr {
 
-unsigned ssm_bwd_take_errors() { return take_errors(); }
+unsigned *ssm_bwd_error_word() { return error_word(); }
 
 static int grad_tile(int S) {
     const int sp = state_pad(S);

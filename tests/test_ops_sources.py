@@ -56,3 +56,10 @@ def test_rows_of_a_norm_in_place(kernel):
     loads = read_only_loads(body(source("group_norm.cu"), kernel))
     assert loads   # the parameters
     assert not [a for a in loads if re.search(r"(?<![\w.])a\.x\b", a)]
+
+
+def test_error_words_are_taken_in_one_step():
+    """Kernels of other streams may set an error bit at any time: a word is cleared by the exchange that
+    reads it, never by a copy after it."""
+    for name in sorted(os.listdir(CSRC)):
+        assert not re.search(r"cudaMemcpy(?:To|From)Symbol(?:Async)?\([^;]*error_word", source(name)), name
