@@ -1,6 +1,9 @@
 """Build the CUDA library in-tree, recurrent_vision_backbone_b200/libgtr_gla.so, and the
 extension module that hands it torch tensors, recurrent_vision_backbone_b200/_ops.so.
 
+The library needs nvcc alone and serves the C ABI by itself; the module (for ``ssm`` and ``norm``) is
+left out, with a note, where torch, g++ or Python's headers are missing.
+
 Compiles the csrc/*.cu sources for sm_100a only (nvcc cross-compiles without a GPU):
     python -m recurrent_vision_backbone_b200.build [--verbose]
 """
@@ -49,6 +52,19 @@ def compile_cmd(src: str, obj: str, extra=()) -> list:
             "-c", src, "-o", obj]
 
 
+def binding_missing() -> str | None:
+    """What the extension module needs and this machine lacks, or None."""
+    try:
+        import torch  # noqa: F401
+    except ImportError:
+        return "torch"
+    if shutil.which("g++") is None:
+        return "g++"
+    if not os.path.exists(os.path.join(sysconfig.get_paths()["include"], "Python.h")):
+        return "Python.h"
+    return None
+
+
 def binding_cmd(out: str) -> list:
     """The command that compiles the extension module against the installed torch and links it to
     the CUDA library beside it."""
@@ -83,6 +99,11 @@ def build(force: bool = False, verbose: bool = False) -> str:
             subprocess.run(nvcc_cmd(tmp, inputs=objs), check=True)
         os.replace(tmp, LIB)
     if force or is_stale(BINDING, BINDING_DEPS):
+        missing = binding_missing()
+        if missing is not None:
+            print(f"{os.path.basename(BINDING)} not built: {missing} is missing (the ssm and norm modules need it)",
+                  file=sys.stderr)
+            return LIB
         tmp = BINDING + ".tmp"
         subprocess.run(binding_cmd(tmp), check=True)
         os.replace(tmp, BINDING)
