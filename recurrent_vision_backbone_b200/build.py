@@ -86,6 +86,20 @@ def is_stale(out: str = LIB, deps=None) -> bool:
     return any(os.path.getmtime(d) > t for d in (DEPS if deps is None else deps))
 
 
+def binding_version() -> str:
+    """What the extension module is compiled against (kept beside it)."""
+    import torch
+    return f"torch {torch.__version__}, Python {sys.version}\n"
+
+
+def binding_is_stale() -> bool:
+    """Whether the extension module is missing, older than its sources or made for another torch or Python."""
+    if is_stale(BINDING, BINDING_DEPS) or not os.path.exists(BINDING + ".version"):
+        return True
+    with open(BINDING + ".version") as f:
+        return f.read() != binding_version()
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     if force or is_stale():
         extra = ["-Xptxas", "-v"] if verbose else []
@@ -98,15 +112,16 @@ def build(force: bool = False, verbose: bool = False) -> str:
                 raise subprocess.CalledProcessError(max(codes, key=abs), "nvcc")
             subprocess.run(nvcc_cmd(tmp, inputs=objs), check=True)
         os.replace(tmp, LIB)
-    if force or is_stale(BINDING, BINDING_DEPS):
-        missing = binding_missing()
-        if missing is not None:
-            print(f"{os.path.basename(BINDING)} not built: {missing} is missing (the ssm and norm modules need it)",
-                  file=sys.stderr)
-            return LIB
+    missing = binding_missing()
+    if missing is not None:
+        print(f"{os.path.basename(BINDING)} not built: {missing} is missing (the ssm and norm modules need it)",
+              file=sys.stderr)
+    elif force or binding_is_stale():
         tmp = BINDING + ".tmp"
         subprocess.run(binding_cmd(tmp), check=True)
         os.replace(tmp, BINDING)
+        with open(BINDING + ".version", "w") as f:
+            f.write(binding_version())
     return LIB
 
 

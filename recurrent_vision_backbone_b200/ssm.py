@@ -27,7 +27,7 @@ def _ops():
         try:
             from . import _ops as m
         except ImportError as e:
-            raise RuntimeError("the extension module is missing: build it with "
+            raise RuntimeError("the extension module is missing or was made for another torch: build it with "
                                "`python -m recurrent_vision_backbone_b200.build`") from e
         _module = m
     return _module

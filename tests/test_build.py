@@ -35,3 +35,18 @@ def test_library_alone(lib, missing, monkeypatch, capfd, tmp_path):
     assert build.build() == lib
     assert missing in capfd.readouterr().err
     assert build.is_stale(build.BINDING, build.BINDING_DEPS)   # a later build makes it
+
+
+def test_extension_module_of_another_torch(lib, monkeypatch):
+    """The module is compiled against torch's headers: with another torch it is built anew."""
+    import torch
+    built = []
+    monkeypatch.setattr(build, "binding_cmd", lambda out: built.append(out) or [sys.executable, "-c", f"open({out!r}, 'w')"])
+    assert build.binding_is_stale()
+    build.build()
+    build.build()
+    assert len(built) == 1 and not build.binding_is_stale()
+    monkeypatch.setattr(torch, "__version__", "1.0.0")
+    assert build.binding_is_stale()
+    build.build()
+    assert len(built) == 2 and not build.binding_is_stale()
