@@ -47,6 +47,11 @@ long long integer(PyObject *o) {
     if (v == -1 && PyErr_Occurred()) throw python_error();
     return v;
 }
+bool truth(PyObject *o) {
+    const int t = PyObject_IsTrue(o);
+    if (t < 0) throw python_error();
+    return t != 0;
+}
 int small(PyObject *o, const char *name) {
     const long long v = integer(o);
     if (v < -0x7fffffffLL || v > 0x7fffffffLL) refuse(std::string(name) + " is out of range");
@@ -214,7 +219,7 @@ PyObject *conv_bwd(PyObject *, PyObject *const *p, Py_ssize_t n) {
     std::vector<Tensor> g = given(p[7], 4);
     if (g.empty())
         g = {c.make({v.B, v.N, v.D}, c.type), c.make({v.D, v.K}, at::kFloat),
-             v.bias ? c.make({v.D}, at::kFloat) : Tensor(), PyObject_IsTrue(p[8]) ? c.make(st, c.type) : Tensor()};
+             v.bias ? c.make({v.D}, at::kFloat) : Tensor(), truth(p[8]) ? c.make(st, c.type) : Tensor()};
     Tensor keep;
     size_t bytes;
     void *ws = c.workspace(p[6], gtr_causal_conv_bwd_workspace_bytes(v.a.B, v.a.Hgrid, v.a.Wgrid, v.a.D, v.a.K), keep, bytes);
@@ -248,9 +253,7 @@ struct Scan {
         a.B = (int)B, a.Hgrid = h, a.Wgrid = v, a.D = (int)C, a.S = (int)S;
         a.direction = small(dir, "direction");
         a.dtype = c.dtype;
-        const int sp = PyObject_IsTrue(softplus);
-        if (sp < 0) throw python_error();
-        a.dt_softplus = sp;
+        a.dt_softplus = truth(softplus);
         a.ldu = c.rows(u, "u", B, N, C);
         a.lddt = c.rows(dt, "dt", B, N, C);
         a.ldb = c.rows(Bm, "Bm", B, N, S);
@@ -299,7 +302,7 @@ PyObject *scan_bwd(PyObject *, PyObject *const *p, Py_ssize_t n) {
     if (g.empty())
         g = {c.make({B, N, C}, c.type), c.make({B, N, C}, c.type), c.make({C, S}, at::kFloat), c.make({B, N, S}, c.type),
              c.make({B, N, S}, c.type), v.D ? c.make({C}, at::kFloat) : Tensor(), v.z ? c.make({B, N, C}, c.type) : Tensor(),
-             v.bias ? c.make({C}, at::kFloat) : Tensor(), PyObject_IsTrue(p[13]) ? c.make({B, C, S}, at::kFloat) : Tensor()};
+             v.bias ? c.make({C}, at::kFloat) : Tensor(), truth(p[13]) ? c.make({B, C, S}, at::kFloat) : Tensor()};
     if (!v.z && g[6].defined()) refuse("grad_z without z");
     gtr_ssm_grads_t o{};
     o.u = c.dense(at_or_none(g[0]), "grad_u", {B, N, C}, c.type, true);
