@@ -194,40 +194,27 @@ __device__ __forceinline__ float ex2(float x) {   // 2^x, about 2 ulp; 0 below 2
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-// log(1 + e) for e in [0, 1]: e times a polynomial of degree 10, interpolating log(1 + e) / e at
-// Chebyshev nodes (relative error 8.5e-10; 1.2e-7 evaluated in float32)
-__device__ __forceinline__ float log1p_01(float e) {
-    float p = 0.001986696617677808f;
-    p = fmaf(p, e, -0.013187826611101627f);
-    p = fmaf(p, e, 0.04100657254457474f);
-    p = fmaf(p, e, -0.08188040554523468f);
-    p = fmaf(p, e, 0.12377995997667313f);
-    p = fmaf(p, e, -0.16087622940540314f);
-    p = fmaf(p, e, 0.19885820150375366f);
-    p = fmaf(p, e, -0.24986496567726135f);
-    p = fmaf(p, e, 0.33332496881484985f);
-    p = fmaf(p, e, -0.4999997913837433f);
-    p = fmaf(p, e, 1.0f);
-    return p * e;
+__device__ __forceinline__ float2 splat(float x) { return make_float2(x, x); }
+__device__ __forceinline__ float horner(float p, float e, float c) { return fmaf(p, e, c); }
+__device__ __forceinline__ float2 horner(float2 p, float2 e, float c) { return __ffma2_rn(p, e, splat(c)); }
+// log(1 + e) / e for e in [0, 1]: a polynomial of degree 10, interpolating at Chebyshev nodes (relative
+// error 8.5e-10; 1.2e-7 evaluated in float32)
+template <typename V>
+__device__ __forceinline__ V log1p_over(V e, V first) {
+    constexpr float c[] = {-0.013187826611101627f, 0.04100657254457474f,  -0.08188040554523468f, 0.12377995997667313f, -0.16087622940540314f,
+                           0.19885820150375366f,   -0.24986496567726135f, 0.33332496881484985f,  -0.4999997913837433f, 1.0f};
+    V p = first;   // the leading coefficient
+#pragma unroll
+    for (int i = 0; i < 10; ++i) p = horner(p, e, c[i]);
+    return p;
 }
+constexpr float kLog1pLead = 0.001986696617677808f;
 // max(x, 0) + log(1 + e^-|x|) of two values at once (packed arithmetic: half the instructions);
 // relative error about |x| 2^-24 from the exponent's rounding, and a NaN stays one (fmaxf alone
 // would drop it)
-__device__ __forceinline__ float2 splat(float x) { return make_float2(x, x); }
 __device__ __forceinline__ float2 softplus_2(float2 x, float2 &e) {   // e: e^-|x|
     e = make_float2(ex2(fabsf(x.x) * -kLog2e), ex2(fabsf(x.y) * -kLog2e));
-    float2 p = splat(0.001986696617677808f);   // log1p_01, twice
-    p = __ffma2_rn(p, e, splat(-0.013187826611101627f));
-    p = __ffma2_rn(p, e, splat(0.04100657254457474f));
-    p = __ffma2_rn(p, e, splat(-0.08188040554523468f));
-    p = __ffma2_rn(p, e, splat(0.12377995967997313f));
-    p = __ffma2_rn(p, e, splat(-0.16087622940540314f));
-    p = __ffma2_rn(p, e, splat(0.19885820150375366f));
-    p = __ffma2_rn(p, e, splat(-0.24986496567726135f));
-    p = __ffma2_rn(p, e, splat(0.33332496881484985f));
-    p = __ffma2_rn(p, e, splat(-0.4999997913837433f));
-    p = __ffma2_rn(p, e, splat(1.0f));
-    return __ffma2_rn(p, e, make_float2(fmaxf(x.x, 0.f), fmaxf(x.y, 0.f)));
+    return __ffma2_rn(log1p_over(e, splat(kLog1pLead)), e, make_float2(fmaxf(x.x, 0.f), fmaxf(x.y, 0.f)));
 }
 __device__ __forceinline__ float rcp_f(float x) {   // 1 / x, about 1 ulp; 0 for infinities
     float y;
@@ -241,7 +228,8 @@ __device__ __forceinline__ float sigmoid_of(float x, float e) {
     return x < 0.f ? e * r : r;
 }
 __device__ __forceinline__ float softplus_f(float x) {
-    return fmaxf(x, 0.f) + log1p_01(ex2(fabsf(x) * -kLog2e));
+    const float e = ex2(fabsf(x) * -kLog2e);
+    return fmaxf(x, 0.f) + log1p_over(e, kLog1pLead) * e;
 }
 
 // ------------------------------------------------------------------ sums over lanes
