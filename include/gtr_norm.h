@@ -1,7 +1,10 @@
 /*
  * gtr_norm.h -- C ABI of the channels-last group norm on B200 (sm_100a), in the same
- * library as gtr_gla.h (libgtr_gla.so): the normalisation of a mixer's output (one group a
- * head) or of a block's input, over the same [B, N, channels] token layout.
+ * library as gtr_gla.h (libgtr_gla.so): the normalisation of a block's input or of a mixer's
+ * output (one group a head) over the tokens of an image, in the same [B, N, channels] layout.
+ * The statistics are over all N tokens: in a causal sequence each result depends on the tokens
+ * behind it.  A norm of each token by itself is the call with the tokens as batch entries of
+ * one row (B = tokens, N = 1).
  *
  *     mean, var over the N tokens and the C / groups channels of a group of one batch entry
  *     (var without Bessel's correction), rstd = 1 / sqrt(var + eps)
@@ -19,12 +22,13 @@
  * enqueued on `stream`, nothing synchronises the host and no call keeps anything.  out may be x
  * itself; nothing else may overlap.  Statistics and sums are held in float32, the variance as
  * parts of (count, mean, squared deviations) that are merged (so a mean far above the spread costs
- * no accuracy), and sums are taken in a fixed order: equal calls give equal bits.  An fp16 output that left the fp16 range (or is
- * NaN) sets GTR_ERR_RANGE in the device error word (gtr_gla_device_status).
+ * no accuracy), and sums are taken in a fixed order: equal calls give equal bits.  An fp16
+ * output that is stored as an infinity or NaN sets GTR_ERR_RANGE in the device error word
+ * (gtr_gla_device_status).
  *   GTR_ERR_INVALID_ARG   null, misaligned, overlapping or negative arguments, groups that do
  *                         not divide C, an eps that is negative or not finite, an unknown type
- *                         or activation, N of 2^30 or more, more than 2^40 elements, a workspace
- *                         that is too small
+ *                         or activation, N of 2^30 or more, B C of 2^31 or more, more than 2^40
+ *                         elements, a workspace that is too small
  *   GTR_ERR_CUDA          a launch failed
  */
 #ifndef GTR_NORM_H
@@ -42,7 +46,7 @@ extern "C" {
 size_t gtr_group_norm_fwd_workspace_bytes(int B, int N, int C, int groups);
 size_t gtr_group_norm_bwd_workspace_bytes(int B, int N, int C, int groups);
 
-/* stats: fully written, or NULL (not wanted).  Without any token nothing is written. */
+/* stats: fully written, or NULL (not wanted).  Without any token nothing is written, stats neither. */
 gtr_status_t gtr_group_norm_fwd(const void *x, const float *gamma, const float *beta, int B, int N, int C, int groups,
                                 float eps, int dtype, int activation, void *out, float *stats, void *workspace,
                                 size_t workspace_bytes, void *stream);

@@ -32,11 +32,13 @@
  * with buffers of their own may run at the same time on several streams.  Outputs and the
  * workspace may not overlap any input or each other, but final_state may be init_state
  * (in-place carry).  States, sums over tokens and softplus are held in float32; each output
- * is rounded once.  An fp16 output that left the fp16 range (or is NaN) sets GTR_ERR_RANGE in the
- * device error word (gtr_gla_device_status); bf16 outputs carry it themselves.
+ * is rounded once.  An fp16 output that is stored as an infinity or NaN sets GTR_ERR_RANGE in the
+ * device error word (gtr_gla_device_status); bf16 outputs carry it themselves.  An infinity or
+ * NaN among the inputs reaches only what the formulas send it to.
  *   GTR_ERR_INVALID_ARG   null, misaligned, overlapping or negative arguments, an unknown
  *                         direction, type or activation, N of 2^30 or more, more than 2^40
- *                         elements in a tensor, a workspace that is too small
+ *                         elements in a tensor, more than a launch's blocks cover (the scan's
+ *                         gradients: B N near 2^29 and up), a workspace that is too small
  *   GTR_ERR_UNSUPPORTED   K outside 2..4; S outside 1..32
  *   GTR_ERR_CUDA          a launch failed
  */

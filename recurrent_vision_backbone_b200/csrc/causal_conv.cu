@@ -78,8 +78,9 @@ static cudaError_t conv_walk(cv::Args a, const ConvPlan &p, bool wide, cudaStrea
 }
 template <typename T, int K>
 static cudaError_t conv_fwd_launch(const cv::Args &a, bool wide, cudaStream_t s) {
-    // the walk once there are chunks of 32 positions for eight blocks an SM: fewer leave the machine to
-    // latency, which the direct kernel meets once a thread
+    // the walk once there are chunks of 32 positions for eight blocks an SM.  us direct / walk, K = 4, inputs in
+    // turn: 4736 x 1024, at the switch, 11.1 / 7.3; 2 x 2304 x 2048 19.2 / 17.0; 8 x 2304 x 2048 67 / 56; below the
+    // switch 4096 x 1024 10.9 / 7.3, and 1600 x 1024 6.5 / 5.7, where the host's time for a call is near
     if ((long long)a.B * ((a.N + 31) / 32) * ((a.D + 127) / 128) >= 148 * 8)
         return conv_walk<T, K>(a, conv_plan(a.B, a.N, a.D, 10), wide, s);
     return wide ? conv_direct<T, 8, K>(a, s) : conv_direct<T, 1, K>(a, s);

@@ -40,7 +40,7 @@ __device__ __forceinline__ Raw<V> early_row(const Args &a, int b, int r, int K, 
 // Few positions.  One thread: V channels, kDirect consecutive scan positions; every row it needs
 // (kDirect + K - 1) is requested before the first is used, so a thread waits for memory once.  Threads
 // run along the channels, so a warp reads whole lines of each row whatever the scan order.  1600
-// tokens of 1024 channels: 8 us with cold caches, latency (6.4 us a call in a row).
+// tokens of 1024 channels: 9 us with cold caches, latency (6 us a call in a row).
 constexpr int kDirect = 4;
 template <typename T, int V, int K>
 __global__ void __launch_bounds__(kThreads, 4) causal_conv_fwd_kernel(const Args a) {
@@ -180,8 +180,9 @@ __device__ __forceinline__ float2 row_pair(const Args &a, int b, int r, int c, b
 }
 
 // Many positions.  A thread walks its chunk with the last K rows of X in registers; rows come two
-// tiles ahead of their use.  8 x 2304 tokens of 2048 channels: 43 us, 3.5 TB/s (51 to 57 with the
-// direct kernel, whose threads wait for memory without work of their own).
+// tiles ahead of their use.  8 x 2304 tokens of 2048 channels: 43 us by itself with cold caches (a third of its
+// writes leave the L2), 56 us a call in a row over inputs beyond L2, 2.7 TB/s (67 with the direct
+// kernel, whose threads wait for memory without work of their own).
 template <typename T, int K, bool WIDE>
 __global__ void __launch_bounds__(kWalkThreads, 10) causal_conv_walk_kernel(const Args a) {
     constexpr int CH = 2 * kWalkThreads;
@@ -267,7 +268,7 @@ __global__ void __launch_bounds__(kWalkThreads, 10) causal_conv_walk_kernel(cons
 // tokens has a fixed order.  Rows come in tiles of kTok tokens through shared memory, as 16-byte
 // asynchronous copies two tiles ahead (element by element where rows do not line up), and leave
 // through it as well: with rows read straight into registers the addresses were half of the
-// instructions (114 us at 8 x 2304 tokens of 2048 channels; 65 so, 3.5 TB/s at 54 % issue).  A tile inside the chunk and the
+// instructions (114 us at 8 x 2304 tokens of 2048 channels; 66 so, 3.4 TB/s at 53 % issue).  A tile inside the chunk and the
 // sequence runs without a branch; the first and the last test every step.
 template <typename T, int K, bool WIDE>
 __global__ void __launch_bounds__(kWalkThreads, 8) causal_conv_bwd_kernel(const Args a) {

@@ -57,7 +57,7 @@ __device__ __forceinline__ float act_grad(float z) {   // silu'(z)
 // time from L2 as far as they fit.  (Holding them on chip in between, the tokens shared out over a
 // cluster's blocks, reads them once but took longer, the blocks of a cluster waiting for one another:
 // 40 us for 26 at 16384 tokens of 1024 channels, 105 for 82 backward at 8 x 2304 of 2048.)  Those
-// two sizes now: 25 us, and 84 us, 4.5 TB/s over both readings.
+// two sizes now: 25 us, and 83 us, 4.5 TB/s over both readings.
 constexpr int kLanes = 8, kEntries = 4;   // tokens in step; entries of a group that a lane joins at most
 struct Piece {
     int first, n, ngroups, cpg;   // the block's first piece, its pieces, its groups, pieces of a group in it

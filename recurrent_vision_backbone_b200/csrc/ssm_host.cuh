@@ -80,8 +80,8 @@ static cudaError_t walk_launch(const sc::Args &a, bool wide, cudaStream_t s) {
         if (pad != sc::kFull) kernel = pad == sc::kQuads ? walk_kernel<T, SP, MODE, SL, sc::kQuads>(wide) : walk_kernel<T, SP, MODE, SL, sc::kAny>(wide);
     }
     // A walk that opens a call and covers many SMs starts plainly: blocks that wait on SMs where the
-    // call ahead happens to have left room end up unevenly spread (468 us for 428 at 8 x 2304 tokens of
-    // 2048 channels)
+    // call ahead happens to have left room end up unevenly spread (381 us for 285 at 8 x 2304 tokens of
+    // 2048 channels; no difference at 6 or 10 x 2304)
     if ((MODE != sc::kOut || a.P == 1) && grid > 148) {
         kernel<<<grid, sc::kThreads, 0, s>>>(a);
         return cudaGetLastError();

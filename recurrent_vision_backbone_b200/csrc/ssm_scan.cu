@@ -9,18 +9,22 @@ namespace gtr {
 
 unsigned *ssm_error_word() { return error_word(); }
 
-constexpr int kSmAim = 148 * 4;   // blocks of four warps that keep the schedulers busy
+constexpr int kSmAim = 148 * 4;   // blocks of four warps that keep the schedulers busy (one wave at up to 16 states)
 
 struct ScanPlan {
     int P, L;
     int SL;   // lanes that share a channel in the walk that writes the outputs
 };
-// The walks of a forward scan.  With 96 blocks of 128 channels or more, one walk over whole
-// sequences: two lanes a channel until the channels alone are three warps a scheduler, then one (8 x 2304
-// tokens of 2048 channels, 128 blocks, at one state of the kernels: 348 us with two lanes, 425 with one, 384
-// with four, 425 in four chunks).  Below that, as many chunks as make one wave of four blocks an SM, at
-// least 32 tokens each (16384 tokens of 1024 channels, 8 blocks: 193 us with 74 chunks, 201 with 92, 250
-// with 37).
+// The walks of a forward scan.  With 96 blocks of 128 channels or more, one walk over whole sequences, with
+// two lanes a channel until the channels alone are three warps a scheduler, then one.  2304 tokens, 16 states,
+// us by blocks: one walk 201 and chunks 204 at 64, 285 and 297 at 90 and at 96, 285 and 355 at 112.  Two lanes
+// and one: 285 and 348 at 96 to 144, 391 and 518 at 160 to 192, 546 and 518 at 224 to 288, 651 and 727 at
+// 320, 766 and 727 at 384, 894 and 924 at 448 (steps where a wave of blocks is full; within 5 % of each
+// other from 224 on but for 320).
+// Fewer blocks: as many chunks as make one wave of four blocks an SM, at least 32 tokens each.  16384 tokens of
+// 1024 channels (8 blocks), us with two, three, four, six blocks an SM: 16 states 230, 209, 182, 185; 8 states
+// 156, 142, 119, 123.  With 17 to 32 states the registers leave two blocks an SM, and four are two waves: 325,
+// 345, 339, 359 at 32 states; at 2048 channels 628, 648, 627, 646.
 static ScanPlan scan_fwd_plan(int B, long long N, int D) {
     const long long base = (long long)B * ((D + sc::kThreads - 1) / sc::kThreads);
     const long long P = base >= 96 ? 1 : kSmAim / base;

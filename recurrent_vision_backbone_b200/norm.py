@@ -21,11 +21,13 @@ def group_norm_bwd_workspace_bytes(B: int, N: int, C: int, groups: int) -> int:
 
 def gtr_group_norm_fwd(x, groups: int, gamma=None, beta=None, eps: float = 1e-5, activation: int = ACT_NONE, out=None,
                        stats=None, workspace=None, stream=None):
-    """act(group_norm(x) gamma + beta) over the tokens and the channels of a group, channels last.
+    """act(group_norm(x) gamma + beta) over the tokens and the channels of a group, channels last (each token
+    by itself: x as [tokens, C]).
 
     x: fp16 or bf16 [B, ..., C], contiguous; gamma, beta: float32 [C] or None; out: a tensor like x to
     fill (x itself for in place) or None; stats: a float32 [B, groups, 2] tensor to fill with the
-    means and reciprocal deviations (the backward pass takes it) or None to allocate one;
+    means and reciprocal deviations (the backward pass takes it; without any token it is left as it
+    is) or None to allocate one;
     workspace: a CUDA tensor of group_norm_fwd_workspace_bytes(...) bytes, or None to allocate one.
     Returns (out, stats)."""
     return _run("norm_fwd", stream, x, gamma, beta, out, stats, workspace, groups, eps, activation)
