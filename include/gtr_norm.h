@@ -27,7 +27,7 @@
  * (gtr_gla_device_status).
  *   GTR_ERR_INVALID_ARG   null, misaligned, overlapping or negative arguments, groups that do
  *                         not divide C, an eps that is negative or not finite, an unknown type
- *                         or activation, N of 2^30 or more, B C of 2^31 or more, more than 2^40
+ *                         or activation, N or C of 2^30 or more, B C of 2^31 or more, more than 2^40
  *                         elements, a workspace that is too small
  *   GTR_ERR_CUDA          a launch failed
  */

@@ -36,7 +36,7 @@
  * device error word (gtr_gla_device_status); bf16 outputs carry it themselves.  An infinity or
  * NaN among the inputs reaches only what the formulas send it to.
  *   GTR_ERR_INVALID_ARG   null, misaligned, overlapping or negative arguments, an unknown
- *                         direction, type or activation, N of 2^30 or more, more than 2^40
+ *                         direction, type or activation, N or D of 2^30 or more, more than 2^40
  *                         elements in a tensor, more than a launch's blocks cover (the scan's
  *                         gradients: B N near 2^29 and up), a workspace that is too small
  *   GTR_ERR_UNSUPPORTED   K outside 2..4; S outside 1..32

@@ -621,7 +621,7 @@ using namespace ops;
 
 static bool bad_sizes(int B, int N, int C, int G) {
     if (B < 0 || N < 0 || C <= 0 || G <= 0 || C % G != 0) return true;
-    return N > kMaxTokens || (long long)B * N > kMaxElements / C || (long long)B * C > 0x7fffffffLL;
+    return N > kMaxTokens || C > kMaxChannels || (long long)B * N > kMaxElements / C || (long long)B * C > 0x7fffffffLL;
 }
 
 struct NormPlan {

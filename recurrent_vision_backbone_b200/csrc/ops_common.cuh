@@ -349,10 +349,11 @@ inline bool overlap(const Span &a, const Span &b) {
 inline long long row_bytes(long long rows, long long ld, long long cols) {
     return rows <= 0 ? 0 : ((rows - 1) * ld + cols) * 2;
 }
-constexpr long long kMaxTokens = (1LL << 30) - 1, kMaxElements = 1LL << 40, kMaxGrid = 0x7fffffffLL;
+// (channels are counted in 32 bits, up to a block's width beyond the last)
+constexpr long long kMaxTokens = (1LL << 30) - 1, kMaxChannels = (1LL << 30) - 1, kMaxElements = 1LL << 40, kMaxGrid = 0x7fffffffLL;
 
 inline bool bad_common(int B, int H, int W, int D, int dir, int dtype) {
-    if (B <= 0 || D <= 0 || H < 0 || W < 0 || dir < 0 || dir > 3) return true;
+    if (B <= 0 || D <= 0 || D > kMaxChannels || H < 0 || W < 0 || dir < 0 || dir > 3) return true;
     if (dtype != GTR_F16 && dtype != GTR_BF16) return true;
     const long long N = (long long)H * W;
     return N > kMaxTokens || (long long)B * N > kMaxElements / D;
