@@ -50,7 +50,11 @@ def test_convolution(B, H, W, D, K, direction, ty, bias, silu, state):
             bounds.check(g, v, e, name)
 
 
-@pytest.mark.parametrize("B,N,C,G,ty,silu,affine,mean", NORM)
+WIDE = [(1, 50, 32768, 1, "fp16", True, True, 0.0),     # a group over 128 blocks, over more than a warp joins, over 17
+        (2, 37, 33000, 1, "bf16", True, True, 0.0), (3, 70, 4112, 1, "fp16", False, True, 0.5)]
+
+
+@pytest.mark.parametrize("B,N,C,G,ty,silu,affine,mean", NORM + WIDE)
 def test_norm(B, N, C, G, ty, silu, affine, mean):
     t = TYPES[ty]
     x, gamma, beta, dy = norm_inputs(B, N, C, t, True, mean, seed=N + C + 1)
