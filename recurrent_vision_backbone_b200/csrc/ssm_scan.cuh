@@ -198,10 +198,11 @@ __global__ void __launch_bounds__(kThreads, walk_blocks<SP, MODE, SL>()) ssm_wal
         float2 y0 = splat(0.f), y1 = splat(0.f);
 #pragma unroll
         for (int q = 0; q < NP / 2; ++q) {
-            // with one lane a channel the first half of the states are never padded, and the group is passed
-            // over; with two, where only the second lane would, it only leaves the sum (passing over it:
-            // 378 us for 285 at 8 x 2304 tokens of 2048 channels, 12 states)
-            const bool maybe = SL > 1 || 4 * q >= SP / 2, in = PAD != kQuads || !maybe || n0 + 4 * q < a.S;
+            // with one lane a channel no state below the group's fewest is padded (of 16: 9, of 8: 4 or 1), and a
+            // group of four is passed over; with two, where only the second lane would, it only leaves the
+            // sum (passing over it: 378 us for 285 at 8 x 2304 tokens of 2048 channels, 12 states)
+            constexpr int real = SL > 1 ? 0 : SP > 8 ? SP / 2 : PAD == kQuads ? 4 : 0;
+            const bool maybe = 4 * q >= real, in = PAD != kQuads || !maybe || n0 + 4 * q < a.S;
             if (SL == 1 && !in) break;
             const float4 Bq = B4[q];
             const float4 Cq = MODE != kLocal ? C4[q] : Bq;

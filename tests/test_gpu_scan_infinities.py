@@ -59,7 +59,8 @@ def plant(c, what, p, d):
 
 # one walk with two lanes a channel and with one, chunks, a single token; states that fill their group and not
 SHAPES = [(1, 37, 40, 5), (1, 37, 40, 16), (2, 150, 33, 12), (1, 40, 31, 20), (1, 9, 3, 1), (97, 5, 6, 11), (450, 3, 5, 5),
-          (2, 1, 20, 11), (2, 1, 20, 16), (97, 9, 40, 12), (450, 5, 16, 24), (1, 70, 128, 4), (3, 50, 7, 8)]
+          (2, 1, 20, 11), (2, 1, 20, 16), (97, 9, 40, 12), (450, 5, 16, 24), (1, 70, 128, 4), (3, 50, 7, 8),
+          (1, 150, 40, 3), (1, 90, 64, 1), (450, 3, 5, 2), (450, 4, 5, 4), (1, 200, 24, 13), (450, 3, 5, 30)]
 
 
 @pytest.mark.parametrize("B,N,D,S", SHAPES)
