@@ -58,7 +58,7 @@ enum { kLocal = 0, kOut = 1, kLocalBwd = 2 };
 
 // States that only fill a kernel's, and how they stay out of the sums over states (their zeros times an
 // infinite step, input or gradient would be no number there).  kFull: there are none.  kQuads: S is
-// a multiple of four, whole groups of four are left out (backward 2 to 5 % of the time, forward none).
+// a multiple of four, whole groups of four are left out (backward up to 3 % of the time, forward none).
 // kAny: values are selected one by one (backward 10 to 14 % at 5 states).
 enum Pad { kFull = 0, kQuads = 1, kAny = 2 };
 

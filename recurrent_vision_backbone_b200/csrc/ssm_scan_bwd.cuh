@@ -79,14 +79,22 @@ __global__ void __launch_bounds__(kThreads, 3) ssm_grad_kernel(const Args a) {
     const bool live = PAD != kQuads || (cv[0] && sl * 4 < a.S);
     const bool two = PAD == kFull || PAIRS || cv[1];
     float *zeros = wsum + 2 * 4 * kSub * 2 * SP + 16;
-    // what this lane reads of a token: its channels' t, x, e, its states' B and C
+    // what this lane reads of a token: its channels' t, x, e, its states' B and C (kQuads: from one place a lane,
+    // chosen once)
+    const float *lane_txe = live ? st + 2 * pr : zeros, *lane_B = live ? sB + sl * 4 : zeros, *lane_C = live ? sC + sl * 4 : zeros;
+    const int lane_step = live ? kSub * SP : 0;
     auto pair_of = [&](const float *p, int tt) {
-        return *reinterpret_cast<const float2 *>(live ? p + tt * CW + 2 * pr : zeros + (p - st) + tt * CW);
+        if constexpr (PAD == kQuads)
+            return *reinterpret_cast<const float2 *>(lane_txe + (p - st) + tt * CW);
+        else
+            return *reinterpret_cast<const float2 *>(p + tt * CW + 2 * pr);
     };
     auto quad_of = [&](const float *p, int s, int tt) {
-        return *reinterpret_cast<const float4 *>(live ? p + (s * kSub + tt) * SP + sl * 4 : zeros + tt * SP);
+        if constexpr (PAD == kQuads)
+            return *reinterpret_cast<const float4 *>((p == sB ? lane_B : lane_C) + s * lane_step + tt * SP);
+        else
+            return *reinterpret_cast<const float4 *>(p + (s * kSub + tt) * SP + sl * 4);
     };
-
     if (PAD == kQuads)
         for (int i = tid; i < Lay::zeros; i += kThreads) zeros[i] = 0.f;
     if (tid < p1 - p0) stok[tid] = token_of(p0 + tid, a.H, a.W, a.dir);
